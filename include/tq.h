@@ -40,7 +40,8 @@
  *    there) and tq_gemv_grouped_prepare.
  *  - Alignment (TQ_ERR_ALIGN otherwise): blobs, tq_pack's trits and
  *    tq_act_quant_int8's x and xq 16 bytes; every other device array 4 bytes
- *    (2 for f16 codebooks).  Outputs must not alias inputs.
+ *    (2 for f16 codebooks), unless the call says otherwise.  Outputs must not
+ *    alias inputs, unless the call says otherwise.
  *  - Argument, shape, alignment and support errors are returned before
  *    anything is enqueued.  A failed launch returns TQ_ERR_DEVICE.  Details
  *    of the last error of the calling thread are in tq_last_error().
@@ -465,6 +466,131 @@ tq_status tq_bitnet_chain_run(const tq_chain_plan* plan, float* x, float* qkv, v
  * resident) -- x is then undefined.
  */
 tq_status tq_bitnet_chain_status(const tq_chain_plan* plan, void* stream);
+
+/*
+ * RMSNorm of a product's output with the residual's addition, to the type
+ * that the next product reads (BitNet's "SubLN Pattern": every ternary linear
+ * reads a normalised input, quantised per token).  Per token m:
+ *   h = x                          without a residual
+ *   h = fl(x + residual)           with one; residual_out (optional) = h,
+ *                                  rounded to residual_type
+ *   r = fl(1 / fl(sqrt(fl(mean + eps)))), mean = sum_i h_i^2 / Kin
+ *   n_i = fl(fl(h_i * r) * weight_i)
+ *   y_type TQ_F32: y = n;   TQ_BF16: y = n rounded to bf16 (nearest even);
+ *   TQ_I8: y and y_scale from n by the rule of tq_act_quant_int8.
+ * The sum of squares is held in fp64 and the mean rounded once to fp32, as in
+ * the decode chain, so the results are those of the same steps done one by
+ * one (only an exact mean within ~1e-14 relative of an fp32 rounding boundary
+ * can differ).  The norm reads h before it is rounded to residual_type.
+ *   x             device [M][Kin] of x_type (TQ_F32 or TQ_BF16), 16-byte aligned
+ *   residual      optional device [M][Kin] of residual_type (TQ_F32 or
+ *                 TQ_BF16), 16-byte aligned
+ *   residual_out  optional device [M][Kin] of residual_type, 16-byte aligned;
+ *                 may be residual itself (the stream updated in place).
+ *                 TQ_ERR_ARG without a residual
+ *   weight        device fp32 [Kin], 16-byte aligned
+ *   y             device [M][Kin] of y_type, 16-byte aligned; with TQ_F32 or
+ *                 TQ_BF16 of x_type it may be x itself
+ *   y_scale       device fp32 [M], TQ_I8 only (else unused)
+ * Other overlaps of an output with another array are refused (TQ_ERR_ARG).
+ * Kin is a multiple of 16, 16 .. 65536; M up to 2^31 - 1 (0 is a no-op);
+ * eps >= 0 and finite (TQ_ERR_VALUE).  Non-finite values follow IEEE
+ * arithmetic to TQ_F32 and TQ_BF16 outputs; to TQ_I8 they leave that token's
+ * y and y_scale unspecified.
+ */
+tq_status tq_rmsnorm(int64_t M, int64_t in_features, int32_t x_type, const void* x, int32_t residual_type,
+                     const void* residual, void* residual_out, const float* weight, float eps, int32_t y_type,
+                     void* y, float* y_scale, void* stream);
+
+/*
+ * Mixture-of-experts rows: the tokens of a batch sorted by expert, so that
+ * each expert's rows are one block (the x of its problems in
+ * tq_gemv_grouped_prepare_tokens, or of a tq_gemm call), and the experts'
+ * outputs brought back to their tokens with the router's weights.
+ *
+ * tq_moe_dispatch: pair p = t * top_k + j is the j-th choice of token t and
+ * belongs to expert experts[t][j]; an id outside 0 .. n_experts - 1 (padding
+ * tokens carry -1) belongs to none.  Pairs are ordered by expert and within
+ * an expert by p (so by token), which places each at a row:
+ *   offsets  device int32 [n_experts + 1]: expert e has the rows offsets[e] ..
+ *            offsets[e + 1] - 1
+ *   rows     device int32 [tokens][top_k]: the pair's row, -1 for no expert
+ *   pairs    device int32 [tokens * top_k]: the row's pair, -1 for the rows
+ *            from offsets[n_experts] on
+ * and, unless x is NULL, copies the rows of x (device [tokens][width] of
+ * x_type TQ_F32, TQ_BF16 or TQ_I8; for TQ_I8 x_scale fp32 [tokens] with them):
+ *   xs       device [tokens * top_k][width] of x_type: xs[rows[t][j]] = x[t]
+ *   xs_scale device fp32 [tokens * top_k], TQ_I8 only
+ * Rows of xs and xs_scale from offsets[n_experts] on are left as they were.
+ * A token may name one expert twice; it then has two rows there.
+ * width is a multiple of 16 up to 65536, x and xs 16-byte aligned; top_k
+ * 1 .. 64, n_experts 1 .. 1024, tokens * top_k up to 2^30.  workspace: device
+ * bytes from tq_moe_dispatch_workspace_size, 16-byte aligned (0 bytes, and
+ * NULL, for few pairs), used by one call at a time: two graphs or streams
+ * that may run at once need one each.  No value of `experts` is read on the
+ * host; the call can be captured.  Outputs must not overlap another array
+ * (TQ_ERR_ARG).
+ */
+tq_status tq_moe_dispatch_workspace_size(int64_t tokens, int32_t top_k, int32_t n_experts, size_t* bytes);
+tq_status tq_moe_dispatch(int64_t tokens, int32_t top_k, int32_t n_experts, const int32_t* experts, int32_t* rows,
+                          int32_t* pairs, int32_t* offsets, int64_t width, int32_t x_type, const void* x,
+                          const float* x_scale, void* xs, float* xs_scale, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   y[t] = sum_j weights[t][j] * ys[rows[t][j]]
+ * in fp32, in the order of j, rounded once to y_type.
+ *   rows     device int32 [tokens][top_k] (from tq_moe_dispatch); a value
+ *            outside 0 .. n_rows - 1 adds nothing, and its weight is not used
+ *   weights  device fp32 [tokens][top_k], or NULL for weights of one (which
+ *            is the gradient of tq_moe_dispatch in x)
+ *   ys       device [n_rows][width] of ys_type (TQ_F32 or TQ_BF16)
+ *   y        device [tokens][width] of y_type (TQ_F32 or TQ_BF16); a token
+ *            without rows gets zeros
+ * Limits as in tq_moe_dispatch, ys and y 16-byte aligned; y must not overlap
+ * another array (TQ_ERR_ARG).
+ */
+tq_status tq_moe_combine(int64_t tokens, int32_t top_k, int64_t width, int64_t n_rows, const int32_t* rows,
+                         const float* weights, int32_t ys_type, const void* ys, int32_t y_type, void* y, void* stream);
+
+/*
+ * The gradient of tq_moe_combine, given dy (device [tokens][width] of dy_type,
+ * TQ_F32 or TQ_BF16):
+ *   d_ys[rows[t][j]] = weights[t][j] * dy[t]     device [n_rows][width] of
+ *                      ys_type, one fp32 product, rounded to ys_type; rows
+ *                      that no pair has are left as they were
+ *   d_weights[t][j]  = sum_i dy[t][i] * ys[rows[t][j]][i]     device fp32
+ *                      [tokens][top_k], summed in fp32 in a fixed order; 0 for a
+ *                      pair without a row
+ * Either output may be NULL (not computed; ys is needed only for d_weights,
+ * weights only for d_ys, where NULL stands for weights of one).  tq_moe_dispatch
+ * gives every pair a row of its own; with other index arrays, a row that
+ * several pairs name is unspecified in d_ys.  Limits and alignment as in tq_moe_combine, d_ys 16-byte
+ * aligned; outputs must not overlap another array (TQ_ERR_ARG).
+ */
+tq_status tq_moe_combine_grad(int64_t tokens, int32_t top_k, int64_t width, int64_t n_rows, const int32_t* rows,
+                              const float* weights, int32_t dy_type, const void* dy, int32_t ys_type, const void* ys,
+                              void* d_ys, float* d_weights, void* stream);
+
+/*
+ * Product of int8 activations with a dense int8 weight, a scale per token and
+ * per output channel -- the linears of a model that are not ternary (output
+ * head, router, attention projections), on the activations that the ternary
+ * products read:
+ *   acc[m][n] = sum_i xq[m][i] * w[n][i]            (int32, exact)
+ *   y[m][n]   = fl(float(acc) * fl(x_scale[m] * w_scale[n]))
+ * then rounded to y_type (TQ_F32, or TQ_BF16 to nearest even): bit exact.
+ *   xq       device int8 [M][Kin], 16-byte aligned (tq_act_quant_int8's or
+ *            tq_rmsnorm's), x_scale device fp32 [M]
+ *   w        device int8 [N][Kin] row-major, every value -128 .. 127, 16-byte
+ *            aligned, w_scale device fp32 [N]
+ *   y        device [M][N] of y_type; must not overlap another array (TQ_ERR_ARG)
+ * Kin is a multiple of 16 up to 65536 (0 gives y = 0 times the scales), N and M up to 2^24;
+ * M = 0 or N = 0 is a no-op.
+ */
+tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t in_features, const int8_t* xq, const float* x_scale,
+                           const int8_t* w, const float* w_scale, int32_t y_type, void* y, void* stream);
 
 #ifdef __cplusplus
 }

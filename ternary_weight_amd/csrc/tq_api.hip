@@ -84,6 +84,16 @@ tq_status tq_check_ptr(const void* p, const char* name, bool nullable, int align
     return TQ_OK;
 }
 
+tq_status tq_check_overlap(const void* out, int64_t out_bytes, const char* out_name, const void* p, int64_t bytes,
+                           const char* name, bool same_ok)
+{
+    if (!out || !p || out_bytes <= 0 || bytes <= 0 || (same_ok && out == p)) return TQ_OK;
+    const uintptr_t a = (uintptr_t)out, b = (uintptr_t)p;
+    if (a < b + (uintptr_t)bytes && b < a + (uintptr_t)out_bytes)
+        return tq_fail(TQ_ERR_ARG, "%s overlaps %s", out_name, name);
+    return TQ_OK;
+}
+
 tq_status tq_check_hip(hipError_t e, const char* what)
 {
     if (e == hipSuccess) return TQ_OK;

@@ -138,3 +138,9 @@ static inline int64_t tq_ws_items_off(int64_t n_probs) { return tq_align256(n_pr
 size_t tq_gemv_lds_bytes(int family, int split_waves, int total_waves, size_t x_lds_bytes);
 // Family id of a (x_type, layout, K, M) combination, or -1 if none.
 int tq_gemv_family(int x_type, int layout, int K, int M);
+
+// TQ_ERR_ARG if the output [out, out + out_bytes) overlaps [p, p + bytes)
+// (either may be null or empty).  `same_ok`: starting at the same address is
+// allowed (an array updated in place).
+tq_status tq_check_overlap(const void* out, int64_t out_bytes, const char* out_name, const void* p, int64_t bytes,
+                           const char* name, bool same_ok = false);
