@@ -13,6 +13,8 @@ namespace {
 using namespace tqk;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 struct Args {
     const int8_t* x;
@@ -59,6 +61,194 @@ __global__ __launch_bounds__(256) void k_dense_i8(Args A, int tiles_m)
     for (int e = 0; e < 4; ++e) store_y<YT>(A, m0 + 4 * q + e, n0 + r, acc[e]);
 }
 
+// ---------------------------------------------------------------------------
+// Tiles through LDS: a workgroup of 4 waves (2 x 2) owns 32 FM tokens by 32 FN
+// rows of w, a wave FM x FN tiles of 16 x 16.
+//
+// A stage is 128 columns (two MFMA steps) of the tile's rows, row-major with
+// 128-byte rows; the 16-byte chunk c of row R sits at slot c ^ (R % 8), so
+// that the 8 lanes of one LDS pass (rows R .. R + 7 of one chunk) fall in
+// distinct banks.  Loads go from memory straight to LDS: a wave's load fills
+// 1 KiB in lane order (8 rows), so the swizzle is applied to the address that
+// each lane reads.  Two stages alternate; while the matrix cores run on one
+// step's fragments those of the next are read from LDS.  At the second step
+// of a stage the waves meet: the next stage has then arrived, and every
+// fragment of this one is in registers, so its place takes the loads of the
+// stage after the next, spread over the step's MFMAs.
+// The first two stages are the last Kin % 256 columns (a whole 256 where that
+// is 0), their x fragments past Kin set to zero, so that the loop needs no
+// masks.  Rows past M and N are read as the last row (their outputs are not
+// stored).
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_u8* dst, uint32_t voff, uint32_t soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
+}
+
+// Wait until at most N of this wave's vector memory operations are pending.
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N < 64, "vmcnt field");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);   // lgkmcnt and expcnt at their maxima
+}
+
+// One MFMA into accumulators that stay in AGPRs in place.  As a builtin, with
+// 256 of them the register allocator moves accumulators between the two
+// register files in the loop (about one move per MFMA).  The s_nop covers a
+// vector instruction that wrote an operand just before (two wait states).
+__device__ __forceinline__ void mfma(i32x4& c, i32x4 a, i32x4 b)
+{
+    asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// The wait states between the last MFMA and the first read of its result.
+__device__ __forceinline__ void mfma_done(i32x4& a, i32x4& b, i32x4& c, i32x4& d)
+{
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(a), "+a"(b), "+a"(c), "+a"(d));
+}
+
+template <int YT, int FM, int FN>
+__global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int tiles_n)
+{
+    constexpr int TM = 32 * FM, TN = 32 * FN, XL = TM / 32, WL = TN / 32, NL = XL + WL;   // loads per wave and stage
+    constexpr int STAGE = (TM + TN) * 128;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE], st1[STAGE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    const int m0 = tm * TM, n0 = tn * TN, K = A.Kin;
+    const int mrows = A.M - m0 < TM ? A.M - m0 : TM, nrows = A.N - n0 < TN ? A.N - n0 : TN;
+    const __amdgpu_buffer_rsrc_t rx = rsrc(A.x + (int64_t)m0 * K, (int64_t)mrows * K);
+    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w + (int64_t)n0 * K, (int64_t)nrows * K);
+
+    // this lane's row in each of the wave's loads (8 rows, 32 apart), and its chunk, the same in all
+    const int c = (lane & 7) ^ (lane >> 3);
+    uint32_t vo[NL];
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+        const int R = ((l < XL ? l : l - XL) * 4 + wave) * 8 + (lane >> 3), rows = l < XL ? mrows : nrows;
+        vo[l] = (uint32_t)(R < rows ? R : rows - 1) * (uint32_t)K;
+    }
+    // the wave's loads l0 .. l1 - 1 of the stage at column `col`; lanes add `off` (their chunk's offset)
+    auto request = [&](uint8_t* st, uint32_t col, uint32_t off, int l0, int l1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int l = l0; l < l1; ++l) {
+            const int id = (l < XL ? l : l - XL) * 4 + wave;
+            load_lds16(l < XL ? rx : rw, (lds_u8*)st + (l < XL ? 0 : TM * 128) + id * 1024, vo[l] + off, col);
+        }
+    };
+    const int at0 = r * 128 + 16 * (q ^ (r & 7)), at1 = at0 ^ 64;      // chunks q and 4 + q of the lane's row
+    const int bx = (wave & 1) * (16 * FM) * 128, bw = TM * 128 + (wave >> 1) * (16 * FN) * 128;
+    i32x4 acc[FN][FM];
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
+    i32x4 fx0[FM], fw0[FN], fx1[FM], fw1[FN];
+    // one step on fragments (x, w); those of the next come from `next` + at.  LOAD: the second step of a stage: the
+    // stage at column `col` is requested into `free`, the place of the step's own
+    auto step = [&](bool load, i32x4 (&x)[FM], i32x4 (&w)[FN], const uint8_t* next, int at, i32x4 (&xn)[FM],
+                    i32x4 (&wn)[FN], uint8_t* free, uint32_t col, uint32_t off) __attribute__((always_inline)) {
+        if (load) {
+            __builtin_amdgcn_s_waitcnt(0x0070);       // vmcnt(0): the next stage's loads; lgkmcnt(0): this one's reads
+            __builtin_amdgcn_s_barrier();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // a row of MFMAs covers the reads of one x and one w fragment and, spread, a load or two: all of a step's
+        // loads at once hold the wave at their issue while its matrix core idles
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+            if (load) request(free, col, off, n * NL / FN, (n + 1) * NL / FN);
+            wn[n] = *(const i32x4*)(next + bw + at + n * 2048);
+#pragma unroll
+            for (int m = n * FM / FN; m < (n + 1) * FM / FN; ++m) xn[m] = *(const i32x4*)(next + bx + at + m * 2048);
+#pragma unroll
+            for (int m = 0; m < FM; ++m) mfma(acc[n][m], w[n], x[m]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto mask = [&](i32x4 (&x)[FM], int left) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < FM; ++m) x[m] = 16 * q < left ? x[m] : i32x4{0, 0, 0, 0};
+    };
+    if (K > 0) {
+        const int tail = (K & 255) ? K & 255 : 256, main = K - tail;     // the first two stages' columns: main ..
+        const int left1 = tail > 128 ? tail - 128 : 0;
+        // chunks past Kin are read from the tail's first one
+        const uint32_t off = 16 * c, offt0 = 16 * c < tail ? 16 * c : 0, offt1 = 16 * c < left1 ? 128 + 16 * c : 0;
+        request(st0, main, offt0, 0, NL);
+        request(st1, main, offt1, 0, NL);
+        wait_vm<NL>();
+        __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int n = 0; n < FN; ++n) fw0[n] = *(const i32x4*)(st0 + bw + at0 + n * 2048);
+#pragma unroll
+        for (int m = 0; m < FM; ++m) fx0[m] = *(const i32x4*)(st0 + bx + at0 + m * 2048);
+        // the tail's four steps; a stage past the last is requested again from column 0 (or is the tail's own)
+        const uint32_t off1 = main > 0 ? off : 0, second = main > 0 ? 128 : 0;
+        mask(fx0, tail);
+        step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
+        mask(fx1, tail - 64);
+        step(true, fx1, fw1, st1, at0, fx0, fw0, st0, 0, off1);
+        mask(fx0, left1);
+        step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
+        mask(fx1, left1 - 64);
+        step(true, fx1, fw1, st0, at0, fx0, fw0, st1, second, off1);
+        for (int k = 0; k < main; k += 256) {
+            const uint32_t next = k + 256 < main ? k + 256 : 0;
+            step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
+            step(true, fx1, fw1, st1, at0, fx0, fw0, st0, next, off);
+            step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
+            step(true, fx1, fw1, st0, at0, fx0, fw0, st1, next + 128, off);
+        }
+        wait_vm<0>();     // the requests past the last stage: no load may land after the workgroup has left
+    }
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; m += 4) mfma_done(acc[n][m], acc[n][m + 1], acc[n][m + 2], acc[n][m + 3]);
+    // lane l holds rows 4 (l / 16) + e of w and token l % 16 of each tile
+    const int mb = m0 + (wave & 1) * (16 * FM) + r, nb = n0 + (wave >> 1) * (16 * FN) + 4 * q;
+    float ws[FN][4], xs[FM];
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ws[n][e] = A.ws[nb + 16 * n + e < A.N ? nb + 16 * n + e : A.N - 1];
+#pragma unroll
+    for (int m = 0; m < FM; ++m) xs[m] = A.xs[mb + 16 * m < A.M ? mb + 16 * m : A.M - 1];
+    // whole tiles with 16-byte (bf16: 8-byte) rows of four outputs, or output by output
+    const bool whole = m0 + TM <= A.M && n0 + TN <= A.N && (A.N & 3) == 0 && ((uintptr_t)A.y & 15) == 0;
+    if (whole) {
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+            for (int n = 0; n < FN; ++n) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = (float)acc[n][m][e] * (xs[m] * ws[n][e]);
+                const int64_t o = (int64_t)(mb + 16 * m) * A.N + nb + 16 * n;
+                if (YT == TQ_F32) *(f32x4*)((float*)A.y + o) = f32x4{v[0], v[1], v[2], v[3]};
+                else *(bf16x4*)((__bf16*)A.y + o) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            }
+    } else {
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+            for (int n = 0; n < FN; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int mm = mb + 16 * m, nn = nb + 16 * n + e;
+                    const float v = (float)acc[n][m][e] * (xs[m] * ws[n][e]);
+                    const int64_t o = (int64_t)mm * A.N + nn;
+                    if (mm < A.M && nn < A.N) {
+                        if (YT == TQ_F32) ((float*)A.y)[o] = v;
+                        else ((__bf16*)A.y)[o] = (__bf16)v;
+                    }
+                }
+    }
+}
+
 }  // namespace
 
 TQ_EXPORT tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t Kin, const int8_t* xq, const float* x_scale,
@@ -85,13 +275,22 @@ TQ_EXPORT tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t Kin, const in
     if ((s = tq_check_overlap(y, yb, "y", x_scale, M * 4, "x_scale"))) return s;
     if ((s = tq_check_overlap(y, yb, "y", w_scale, N * 4, "w_scale"))) return s;
     const Args A{xq, x_scale, w, w_scale, y, (int32_t)M, (int32_t)N, (int32_t)Kin};
-    const int64_t tm = (M + 15) / 16, tn = (N + 63) / 64;
-    if (tm * tn > (1 << 24) - 1)
-        return tq_fail(TQ_ERR_UNSUPPORTED, "%lld tiles exceed one launch", (long long)(tm * tn));
-    if (y_type == TQ_F32)
-        hipLaunchKernelGGL(k_dense_i8<TQ_F32>, dim3((unsigned)(tm * tn)), dim3(256), 0, (hipStream_t)stream, A, (int)tm);
-    else
-        hipLaunchKernelGGL(k_dense_i8<TQ_BF16>, dim3((unsigned)(tm * tn)), dim3(256), 0, (hipStream_t)stream, A, (int)tm);
+    hipStream_t st = (hipStream_t)stream;
+    const auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+    if (M > 64) {
+        if (tiles(256, 256) > INT32_MAX / 256)
+            return tq_fail(TQ_ERR_UNSUPPORTED, "%lld tiles exceed one launch", (long long)tiles(256, 256));
+        const int tm = (int)((M + 255) / 256), tn = (int)((N + 32*8-1) / (32*8));
+        if (y_type == TQ_F32)
+            hipLaunchKernelGGL((k_dense_i8_tile<TQ_F32, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
+        else
+            hipLaunchKernelGGL((k_dense_i8_tile<TQ_BF16, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
+    } else {
+        const int tm = (int)((M + 15) / 16);
+        const dim3 grid((unsigned)tiles(16, 64));
+        if (y_type == TQ_F32) hipLaunchKernelGGL(k_dense_i8<TQ_F32>, grid, dim3(256), 0, st, A, tm);
+        else hipLaunchKernelGGL(k_dense_i8<TQ_BF16>, grid, dim3(256), 0, st, A, tm);
+    }
     if ((s = tq_check_launch("tq_gemm_dense_i8"))) return s;
     return tq_ok();
 }
