@@ -13,8 +13,8 @@ namespace {
 using namespace tqk;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 bf16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 
 struct Args {
     const int8_t* x;
@@ -25,40 +25,107 @@ struct Args {
     int32_t M, N, Kin;
 };
 
+// Four outputs of a row, `left` of them (at least one) inside it.  Rows start
+// on any 4 bytes (bf16: 2): one store of 16 (8) bytes needs no more than that.
 template <int YT>
-__device__ __forceinline__ void store_y(const Args& A, int m, int n, int acc)
+__device__ __forceinline__ void store_quad(void* y, int64_t at, const float (&v)[4], int left)
 {
-    if (m >= A.M || n >= A.N) return;
-    const float v = (float)acc * (A.xs[m] * A.ws[n]);
-    const int64_t at = (int64_t)m * A.N + n;
-    if (YT == TQ_F32) ((float*)A.y)[at] = v;
-    else ((__bf16*)A.y)[at] = (__bf16)v;
+    if (left >= 4) {
+        if (YT == TQ_F32) *(f32x4_u*)((float*)y + at) = f32x4_u{v[0], v[1], v[2], v[3]};
+        else *(bf16x4_u*)((__bf16*)y + at) = bf16x4_u{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < left) {
+            if (YT == TQ_F32) ((float*)y)[at + e] = v[e];
+            else ((__bf16*)y)[at + e] = (__bf16)v[e];
+        }
 }
 
-// A workgroup of 4 waves: 16 tokens by 64 rows of w, a 16 x 16 tile per wave.
-// Lane l holds 16 columns of row l % 16 per operand and step of 64 columns.
-// Buffer resources: rows past M and N, and columns past Kin, read zeros.
-template <int YT>
-__global__ __launch_bounds__(256) void k_dense_i8(Args A, int tiles_m)
+// ---------------------------------------------------------------------------
+// Few tokens: the weight is read once, straight into MFMA operands.  A wave
+// owns 16 RT rows of w and 16 MT tokens; W waves split the columns, 128 at a
+// time in turn, and add their sums in LDS (integers: any order).  G such
+// groups make a workgroup.  A unit of 128 columns is a whole line of each row
+// (two MFMA steps); D units per wave are in flight.  Loads go through buffer
+// resources: lanes past M, N or Kin read zeros without touching memory.
+template <int YT, int MT, int RT, int W, int G, int D>
+__global__ __launch_bounds__(64 * W * G) void k_dense_i8_few(Args A, int blocks_m)
 {
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int m0 = (int)(blockIdx.x % tiles_m) * 16, n0 = (int)(blockIdx.x / tiles_m) * 64 + (threadIdx.x >> 6) * 16;
-    if (n0 >= A.N) return;
-    const int K = A.Kin;
-    const int64_t mrows = A.M - m0 < 16 ? A.M - m0 : 16, nrows = A.N - n0 < 16 ? A.N - n0 : 16;
-    const __amdgpu_buffer_rsrc_t rx = rsrc(A.x + (int64_t)m0 * K, mrows * K);
-    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w + (int64_t)n0 * K, nrows * K);
-    i32x4 acc = {0, 0, 0, 0};
-    for (int k = 0; k < K; k += 64) {
-        const int c = k + 16 * q;
-        const uint32_t off = c < K ? (uint32_t)(r * K + c) : kOffNone;
-        const u32x4 a = buffer_load<u32x4, 0>(rx, off, 0), b = buffer_load<u32x4, 0>(rw, off, 0);
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), acc, 0,
-                                                    0, 0);
-    }
-    // lane l holds column l % 16 (n) of rows 4 (l / 16) + e (m)
+    __shared__ i32x4 red[W > 1 ? G : 1][W > 1 ? W : 1][W > 1 ? RT * MT : 1][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    const int g = wave / W, part = wave % W;
+    const int m0 = (int)(blockIdx.x % blocks_m) * 16 * MT, n0 = ((int)(blockIdx.x / blocks_m) * G + g) * 16 * RT;
+    const int K = A.Kin, U = (K + 127) >> 7;
+    const int mrows = A.M - m0 < 16 * MT ? A.M - m0 : 16 * MT;
+    const int nrows = n0 >= A.N ? 0 : A.N - n0 < 16 * RT ? A.N - n0 : 16 * RT;
+    const __amdgpu_buffer_rsrc_t rx = rsrc(A.x + (int64_t)m0 * K, (int64_t)mrows * K);
+    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w + (int64_t)(nrows ? n0 : 0) * K, (int64_t)nrows * K);
+    uint32_t xo[MT], wo[RT];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) store_y<YT>(A, m0 + 4 * q + e, n0 + r, acc[e]);
+    for (int m = 0; m < MT; ++m) xo[m] = 16 * m + r < mrows ? (uint32_t)(16 * m + r) * (uint32_t)K + 16 * q : kOffNone;
+#pragma unroll
+    for (int n = 0; n < RT; ++n) wo[n] = 16 * n + r < nrows ? (uint32_t)(16 * n + r) * (uint32_t)K + 16 * q : kOffNone;
+    i32x4 acc[RT][MT];
+#pragma unroll
+    for (int n = 0; n < RT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
+    u32x4 fx[D][2][MT], fw[D][2][RT];
+    auto load = [&](int d, int u) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int col = u * 128 + h * 64;
+            const bool in = col + 16 * q < K;             // also false past the last unit
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+                fw[d][h][n] = buffer_load<u32x4, kCacheNT>(rw, in ? wo[n] + col : kOffNone, 0);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fx[d][h][m] = buffer_load<u32x4, 0>(rx, in ? xo[m] + col : kOffNone, 0);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, part + d * W);
+    for (int u = part; u < U; u += D * W) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[n][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fw[d][h][n]),
+                                                                          __builtin_bit_cast(i32x4, fx[d][h][m]),
+                                                                          acc[n][m], 0, 0, 0);
+            load(d, u + (d + D) * W);
+        }
+    }
+    // lane l holds rows 4 (l / 16) + e of w and token l % 16 of each tile
+    auto store = [&](int t, i32x4 v) __attribute__((always_inline)) {
+        const int mm = m0 + 16 * (t % MT) + r, nn = n0 + 16 * (t / MT) + 4 * q;
+        if (mm >= A.M || nn >= A.N) return;
+        const float xs = A.xs[mm];
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * (xs * A.ws[nn + e < A.N ? nn + e : A.N - 1]);
+        store_quad<YT>(A.y, (int64_t)mm * A.N + nn, f, A.N - nn);
+    };
+    if constexpr (W == 1) {
+#pragma unroll
+        for (int t = 0; t < RT * MT; ++t) store(t, acc[t / MT][t % MT]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < RT * MT; ++t) red[g][part][t][lane] = acc[t / MT][t % MT];
+        __syncthreads();
+        for (int t = part; t < RT * MT; t += W) {
+            i32x4 v = red[g][0][t][lane];
+#pragma unroll
+            for (int p = 1; p < W; ++p) v += red[g][p][t][lane];
+            store(t, v);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -109,6 +176,21 @@ __device__ __forceinline__ void mfma_done(i32x4& a, i32x4& b, i32x4& c, i32x4& d
     asm volatile("s_nop 15\n\ts_nop 15" : "+a"(a), "+a"(b), "+a"(c), "+a"(d));
 }
 
+// Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of the
+// tiles, in strips of kStrip tiles of tokens walked column by column, so that
+// its 32 concurrent tiles share few rows of x and w in its L2 (2048 x 6912 x
+// 2560: 44.2 -> 41.5 us; strips of 2 or 8 measured alike).
+constexpr int kStrip = 4;
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* tm, int* tn)
+{
+    const int total = tiles_m * tiles_n, per = total >> 3, rem = total & 7, xcd = id & 7;
+    const int s = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+    const int strip = s / (kStrip * tiles_n), left = tiles_m - strip * kStrip, wide = left < kStrip ? left : kStrip;
+    const int in = s - strip * kStrip * tiles_n;
+    *tm = strip * kStrip + in % wide;
+    *tn = in / wide;
+}
+
 template <int YT, int FM, int FN>
 __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int tiles_n)
 {
@@ -116,7 +198,8 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
     constexpr int STAGE = (TM + TN) * 128;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE], st1[STAGE];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    int tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
     const int m0 = tm * TM, n0 = tn * TN, K = A.Kin;
     const int mrows = A.M - m0 < TM ? A.M - m0 : TM, nrows = A.N - n0 < TN ? A.N - n0 : TN;
     const __amdgpu_buffer_rsrc_t rx = rsrc(A.x + (int64_t)m0 * K, (int64_t)mrows * K);
@@ -217,36 +300,60 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
         for (int e = 0; e < 4; ++e) ws[n][e] = A.ws[nb + 16 * n + e < A.N ? nb + 16 * n + e : A.N - 1];
 #pragma unroll
     for (int m = 0; m < FM; ++m) xs[m] = A.xs[mb + 16 * m < A.M ? mb + 16 * m : A.M - 1];
-    // whole tiles with 16-byte (bf16: 8-byte) rows of four outputs, or output by output
-    const bool whole = m0 + TM <= A.M && n0 + TN <= A.N && (A.N & 3) == 0 && ((uintptr_t)A.y & 15) == 0;
-    if (whole) {
+    auto store = [&](int m, int n, int left) __attribute__((always_inline)) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[n][m][e] * (xs[m] * ws[n][e]);
+        store_quad<YT>(A.y, (int64_t)(mb + 16 * m) * A.N + nb + 16 * n, v, left);
+    };
+    if (n0 + TN <= A.N) {                                    // tests per four outputs cost 7 us on 4096 x 4096
 #pragma unroll
         for (int m = 0; m < FM; ++m)
+            if (mb + 16 * m < A.M)
 #pragma unroll
-            for (int n = 0; n < FN; ++n) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = (float)acc[n][m][e] * (xs[m] * ws[n][e]);
-                const int64_t o = (int64_t)(mb + 16 * m) * A.N + nb + 16 * n;
-                if (YT == TQ_F32) *(f32x4*)((float*)A.y + o) = f32x4{v[0], v[1], v[2], v[3]};
-                else *(bf16x4*)((__bf16*)A.y + o) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-            }
+                for (int n = 0; n < FN; ++n) store(m, n, 4);
     } else {
 #pragma unroll
-        for (int m = 0; m < FM; ++m)
+        for (int n = 0; n < FN; ++n) {
+            const int left = A.N - (nb + 16 * n);
+            if (left > 0)
 #pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int mm = mb + 16 * m, nn = nb + 16 * n + e;
-                    const float v = (float)acc[n][m][e] * (xs[m] * ws[n][e]);
-                    const int64_t o = (int64_t)mm * A.N + nn;
-                    if (mm < A.M && nn < A.N) {
-                        if (YT == TQ_F32) ((float*)A.y)[o] = v;
-                        else ((__bf16*)A.y)[o] = (__bf16)v;
-                    }
-                }
+                for (int m = 0; m < FM; ++m)
+                    if (mb + 16 * m < A.M) store(m, n, left);
+        }
     }
+}
+
+#ifndef FEW_MT1
+#define FEW_MT1
+#endif
+
+template <int YT, int MT, int RT, int W, int G, int D>
+tq_status launch_few_as(const Args& A, hipStream_t st)
+{
+    const int64_t bm = (A.M + 16 * MT - 1) / (16 * MT), bn = (A.N + 16 * RT * G - 1) / (16 * RT * G);
+    if (bm * bn * 64 * W * G > UINT32_MAX)
+        return tq_fail(TQ_ERR_UNSUPPORTED, "%lld tiles exceed one launch", (long long)(bm * bn));
+    hipLaunchKernelGGL((k_dense_i8_few<YT, MT, RT, W, G, D>), dim3((unsigned)(bm * bn)), dim3(64 * W * G), 0, st, A, (int)bm);
+    return TQ_OK;
+}
+
+template <int YT, int MT>
+tq_status launch_few_m(const Args& A, hipStream_t st)
+{
+    constexpr int D = MT == 1 ? 4 : MT == 2 ? 3 : 2;
+    const int64_t rows = (A.N + 15) / 16;           // 16-row tiles
+    if (rows <= 1024) return launch_few_as<YT, MT, 1, 8, 1, D>(A, st);
+    if (rows <= 4096) return launch_few_as<YT, MT, 1, 4, 1, D>(A, st);
+    return launch_few_as<YT, MT, 1, 2, 2, D>(A, st);
+}
+
+template <int YT>
+tq_status launch_few(const Args& A, hipStream_t st)
+{
+    if (A.M <= 16) return launch_few_m<YT, 1>(A, st);
+    if (A.M <= 32) return launch_few_m<YT, 2>(A, st);
+    return launch_few_m<YT, 4>(A, st);
 }
 
 }  // namespace
@@ -285,11 +392,8 @@ TQ_EXPORT tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t Kin, const in
             hipLaunchKernelGGL((k_dense_i8_tile<TQ_F32, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
         else
             hipLaunchKernelGGL((k_dense_i8_tile<TQ_BF16, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
-    } else {
-        const int tm = (int)((M + 15) / 16);
-        const dim3 grid((unsigned)tiles(16, 64));
-        if (y_type == TQ_F32) hipLaunchKernelGGL(k_dense_i8<TQ_F32>, grid, dim3(256), 0, st, A, tm);
-        else hipLaunchKernelGGL(k_dense_i8<TQ_BF16>, grid, dim3(256), 0, st, A, tm);
+    } else if ((s = y_type == TQ_F32 ? launch_few<TQ_F32>(A, st) : launch_few<TQ_BF16>(A, st))) {
+        return s;
     }
     if ((s = tq_check_launch("tq_gemm_dense_i8"))) return s;
     return tq_ok();
