@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * W * G) void k_dense_i8_few(Args A, int blocks_
             const bool in = col + 16 * q < K;             // also false past the last unit
 #pragma unroll
             for (int n = 0; n < RT; ++n)
-                fw[d][h][n] = buffer_load<u32x4, kCacheNT>(rw, in ? wo[n] + col : kOffNone, 0);
+                fw[d][h][n] = buffer_load<u32x4, 0>(rw, in ? wo[n] + col : kOffNone, 0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) fx[d][h][m] = buffer_load<u32x4, 0>(rx, in ? xo[m] + col : kOffNone, 0);
         }
@@ -168,12 +168,6 @@ __device__ __forceinline__ void wait_vm()
 __device__ __forceinline__ void mfma(i32x4& c, i32x4 a, i32x4 b)
 {
     asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-
-// The wait states between the last MFMA and the first read of its result.
-__device__ __forceinline__ void mfma_done(i32x4& a, i32x4& b, i32x4& c, i32x4& d)
-{
-    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(a), "+a"(b), "+a"(c), "+a"(d));
 }
 
 // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of the
@@ -287,10 +281,12 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
         }
         wait_vm<0>();     // the requests past the last stage: no load may land after the workgroup has left
     }
+    // the wait states between the last MFMA and the first read of a result; the reads stay behind it
+    asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
     for (int n = 0; n < FN; ++n)
 #pragma unroll
-        for (int m = 0; m < FM; m += 4) mfma_done(acc[n][m], acc[n][m + 1], acc[n][m + 2], acc[n][m + 3]);
+        for (int m = 0; m < FM; ++m) asm volatile("" : "+a"(acc[n][m]));
     // lane l holds rows 4 (l / 16) + e of w and token l % 16 of each tile
     const int mb = m0 + (wave & 1) * (16 * FM) + r, nb = n0 + (wave >> 1) * (16 * FN) + 4 * q;
     float ws[FN][4], xs[FM];
