@@ -5,6 +5,8 @@
 //   y = fl(float(acc) fl(x_scale[m] w_scale[n])).
 //
 // |acc| <= 128 * 128 * 65536 = 2^30, so int32 never wraps.
+#include <math.h>
+
 #include "tq_internal.h"
 #include "tq_decode.h"
 
@@ -44,45 +46,37 @@ __device__ __forceinline__ void store_quad(void* y, int64_t at, const float (&v)
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the weight is read once, straight into MFMA operands.  A wave
-// owns 16 RT rows of w and 16 MT tokens; W waves split the columns, 128 at a
-// time in turn, and add their sums in LDS (integers: any order).  G such
-// groups make a workgroup.  A unit of 128 columns is a whole line of each row
-// (two MFMA steps); D units per wave are in flight.  Loads go through buffer
-// resources: lanes past M, N or Kin read zeros without touching memory.
-template <int YT, int MT, int RT, int W, int G, int D>
-__global__ __launch_bounds__(64 * W * G) void k_dense_i8_few(Args A, int blocks_m)
+// A few tokens against a narrow weight (M <= 16): too few tiles to fill the
+// GPU, so W waves split a 16 x 16 tile's columns, 128 at a time in turn (a
+// whole line of each row: two MFMA steps), and add their sums in LDS
+// (integers: any order gives the same).  The weight goes from memory straight
+// into MFMA operands, two units per wave in flight (four were slower: the
+// waves of a compute unit together hold enough); non-temporal loads were 10%
+// slower.  Loads go through buffer resources: lanes past M, N or Kin read
+// zeros without touching memory.
+// 13 x 4096 x 14336: 17.9 us, 3.3 TB/s.
+template <int YT, int W>
+__global__ __launch_bounds__(64 * W) void k_dense_i8_few(Args A, int tiles_m, int)
 {
-    __shared__ i32x4 red[W > 1 ? G : 1][W > 1 ? W : 1][W > 1 ? RT * MT : 1][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-    const int g = wave / W, part = wave % W;
-    const int m0 = (int)(blockIdx.x % blocks_m) * 16 * MT, n0 = ((int)(blockIdx.x / blocks_m) * G + g) * 16 * RT;
+    constexpr int D = 2;
+    __shared__ i32x4 red[W][64];
+    const int lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    const int m0 = (int)(blockIdx.x % tiles_m) * 16, n0 = (int)(blockIdx.x / tiles_m) * 16;
     const int K = A.Kin, U = (K + 127) >> 7;
-    const int mrows = A.M - m0 < 16 * MT ? A.M - m0 : 16 * MT;
-    const int nrows = n0 >= A.N ? 0 : A.N - n0 < 16 * RT ? A.N - n0 : 16 * RT;
+    const int mrows = A.M - m0 < 16 ? A.M - m0 : 16, nrows = A.N - n0 < 16 ? A.N - n0 : 16;
     const __amdgpu_buffer_rsrc_t rx = rsrc(A.x + (int64_t)m0 * K, (int64_t)mrows * K);
-    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w + (int64_t)(nrows ? n0 : 0) * K, (int64_t)nrows * K);
-    uint32_t xo[MT], wo[RT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) xo[m] = 16 * m + r < mrows ? (uint32_t)(16 * m + r) * (uint32_t)K + 16 * q : kOffNone;
-#pragma unroll
-    for (int n = 0; n < RT; ++n) wo[n] = 16 * n + r < nrows ? (uint32_t)(16 * n + r) * (uint32_t)K + 16 * q : kOffNone;
-    i32x4 acc[RT][MT];
-#pragma unroll
-    for (int n = 0; n < RT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
-    u32x4 fx[D][2][MT], fw[D][2][RT];
+    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w + (int64_t)n0 * K, (int64_t)nrows * K);
+    const uint32_t xo = r < mrows ? (uint32_t)r * (uint32_t)K + 16 * q : kOffNone;
+    const uint32_t wo = r < nrows ? (uint32_t)r * (uint32_t)K + 16 * q : kOffNone;
+    i32x4 acc = {0, 0, 0, 0};
+    u32x4 fx[D][2], fw[D][2];
     auto load = [&](int d, int u) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int col = u * 128 + h * 64;
             const bool in = col + 16 * q < K;             // also false past the last unit
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-                fw[d][h][n] = buffer_load<u32x4, 0>(rw, in ? wo[n] + col : kOffNone, 0);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) fx[d][h][m] = buffer_load<u32x4, 0>(rx, in ? xo[m] + col : kOffNone, 0);
+            fw[d][h] = buffer_load<u32x4, 0>(rw, in ? wo + col : kOffNone, 0);
+            fx[d][h] = buffer_load<u32x4, 0>(rx, in ? xo + col : kOffNone, 0);
         }
     };
 #pragma unroll
@@ -92,40 +86,25 @@ __global__ __launch_bounds__(64 * W * G) void k_dense_i8_few(Args A, int blocks_
         for (int d = 0; d < D; ++d) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < RT; ++n)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        acc[n][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fw[d][h][n]),
-                                                                          __builtin_bit_cast(i32x4, fx[d][h][m]),
-                                                                          acc[n][m], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fw[d][h]),
+                                                            __builtin_bit_cast(i32x4, fx[d][h]), acc, 0, 0, 0);
             load(d, u + (d + D) * W);
         }
     }
-    // lane l holds rows 4 (l / 16) + e of w and token l % 16 of each tile
-    auto store = [&](int t, i32x4 v) __attribute__((always_inline)) {
-        const int mm = m0 + 16 * (t % MT) + r, nn = n0 + 16 * (t / MT) + 4 * q;
-        if (mm >= A.M || nn >= A.N) return;
-        const float xs = A.xs[mm];
-        float f[4];
+    red[part][lane] = acc;
+    __syncthreads();
+    if (part != 0) return;
+    // lane l holds rows 4 (l / 16) + e of w and token l % 16
+    i32x4 sum = red[0][lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * (xs * A.ws[nn + e < A.N ? nn + e : A.N - 1]);
-        store_quad<YT>(A.y, (int64_t)mm * A.N + nn, f, A.N - nn);
-    };
-    if constexpr (W == 1) {
+    for (int p = 1; p < W; ++p) sum += red[p][lane];
+    const int m = m0 + r, n = n0 + 4 * q;
+    if (m >= A.M || n >= A.N) return;
+    const float xs = A.xs[m];
+    float v[4];
 #pragma unroll
-        for (int t = 0; t < RT * MT; ++t) store(t, acc[t / MT][t % MT]);
-    } else {
-#pragma unroll
-        for (int t = 0; t < RT * MT; ++t) red[g][part][t][lane] = acc[t / MT][t % MT];
-        __syncthreads();
-        for (int t = part; t < RT * MT; t += W) {
-            i32x4 v = red[g][0][t][lane];
-#pragma unroll
-            for (int p = 1; p < W; ++p) v += red[g][p][t][lane];
-            store(t, v);
-        }
-    }
+    for (int e = 0; e < 4; ++e) v[e] = (float)sum[e] * (xs * A.ws[n + e < A.N ? n + e : A.N - 1]);
+    store_quad<YT>(A.y, (int64_t)m * A.N + n, v, A.N - n);
 }
 
 // ---------------------------------------------------------------------------
@@ -161,15 +140,6 @@ __device__ __forceinline__ void wait_vm()
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);   // lgkmcnt and expcnt at their maxima
 }
 
-// One MFMA into accumulators that stay in AGPRs in place.  As a builtin, with
-// 256 of them the register allocator moves accumulators between the two
-// register files in the loop (about one move per MFMA).  The s_nop covers a
-// vector instruction that wrote an operand just before (two wait states).
-__device__ __forceinline__ void mfma(i32x4& c, i32x4 a, i32x4 b)
-{
-    asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-
 // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of the
 // tiles, in strips of kStrip tiles of tokens walked column by column, so that
 // its 32 concurrent tiles share few rows of x and w in its L2 (2048 x 6912 x
@@ -185,13 +155,16 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
     *tn = in / wide;
 }
 
-template <int YT, int FM, int FN>
-__global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int tiles_n)
+template <int YT, int FM, int FN, int KS>
+__global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m, int tiles_n)
 {
     constexpr int TM = 32 * FM, TN = 32 * FN, XL = TM / 32, WL = TN / 32, NL = XL + WL;   // loads per wave and stage
     constexpr int STAGE = (TM + TN) * 128;
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE], st1[STAGE];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0_[KS * STAGE], st1_[KS * STAGE];
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave_id & 3, group = wave_id >> 2;
+    uint8_t* const st0 = st0_ + group * STAGE;
+    uint8_t* const st1 = st1_ + group * STAGE;
     int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
     const int m0 = tm * TM, n0 = tn * TN, K = A.Kin;
@@ -241,7 +214,8 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
 #pragma unroll
             for (int m = n * FM / FN; m < (n + 1) * FM / FN; ++m) xn[m] = *(const i32x4*)(next + bx + at + m * 2048);
 #pragma unroll
-            for (int m = 0; m < FM; ++m) mfma(acc[n][m], w[n], x[m]);
+            for (int m = 0; m < FM; ++m)
+                acc[n][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[n], x[m], acc[n][m], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -250,43 +224,69 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
         for (int m = 0; m < FM; ++m) x[m] = 16 * q < left ? x[m] : i32x4{0, 0, 0, 0};
     };
     if (K > 0) {
-        const int tail = (K & 255) ? K & 255 : 256, main = K - tail;     // the first two stages' columns: main ..
+        // 256 columns at a time, dealt to the groups in turn from the end: `first` may be short, or past Kin and empty
+        const int chunks = (K + 255) >> 8, turns = (chunks + KS - 1) / KS;
+        const int first = ((turns - 1) * KS + group) * 256, tail = K - first < 0 ? 0 : K - first < 256 ? K - first : 256;
         const int left1 = tail > 128 ? tail - 128 : 0;
-        // chunks past Kin are read from the tail's first one
-        const uint32_t off = 16 * c, offt0 = 16 * c < tail ? 16 * c : 0, offt1 = 16 * c < left1 ? 128 + 16 * c : 0;
-        request(st0, main, offt0, 0, NL);
-        request(st1, main, offt1, 0, NL);
+        // chunks past Kin are read from column 0
+        const uint32_t off = 16 * c, offt0 = 16 * c < tail ? first + 16 * c : 0, offt1 = 16 * c < left1 ? first + 128 + 16 * c : 0;
+        request(st0, 0, offt0, 0, NL);
+        request(st1, 0, offt1, 0, NL);
         wait_vm<NL>();
         __builtin_amdgcn_s_barrier();
 #pragma unroll
         for (int n = 0; n < FN; ++n) fw0[n] = *(const i32x4*)(st0 + bw + at0 + n * 2048);
 #pragma unroll
         for (int m = 0; m < FM; ++m) fx0[m] = *(const i32x4*)(st0 + bx + at0 + m * 2048);
-        // the tail's four steps; a stage past the last is requested again from column 0 (or is the tail's own)
-        const uint32_t off1 = main > 0 ? off : 0, second = main > 0 ? 128 : 0;
+        // the four steps of `first`; a stage past the group's last is requested again from column 0
+        const bool more = turns > 1;
+        const uint32_t off1 = more ? off : 0;
+        int k = more ? first - KS * 256 : 0;
         mask(fx0, tail);
         step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
         mask(fx1, tail - 64);
-        step(true, fx1, fw1, st1, at0, fx0, fw0, st0, 0, off1);
+        step(true, fx1, fw1, st1, at0, fx0, fw0, st0, k, off1);
         mask(fx0, left1);
         step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
         mask(fx1, left1 - 64);
-        step(true, fx1, fw1, st0, at0, fx0, fw0, st1, second, off1);
-        for (int k = 0; k < main; k += 256) {
-            const uint32_t next = k + 256 < main ? k + 256 : 0;
+        step(true, fx1, fw1, st0, at0, fx0, fw0, st1, k + (more ? 128 : 0), off1);
+        for (int i = 1; i < turns; ++i) {
+            k = k >= KS * 256 ? k - KS * 256 : 0;
             step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
-            step(true, fx1, fw1, st1, at0, fx0, fw0, st0, next, off);
+            step(true, fx1, fw1, st1, at0, fx0, fw0, st0, k, off);
             step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
-            step(true, fx1, fw1, st0, at0, fx0, fw0, st1, next + 128, off);
+            step(true, fx1, fw1, st0, at0, fx0, fw0, st1, k + 128, off);
         }
         wait_vm<0>();     // the requests past the last stage: no load may land after the workgroup has left
     }
-    // the wait states between the last MFMA and the first read of a result; the reads stay behind it
-    asm volatile("s_nop 15\n\ts_nop 15");
+    if constexpr (KS > 1) {
+        // the groups' sums meet in the stages' place (even tiles in the first's, odd ones in the second's): group g
+        // adds up and stores the tiles g, g + KS, ..
+        constexpr int HT = (FM * FN + 1) / 2;
+        static_assert(4 * HT * 1024 <= STAGE, "partial sums fit the stages");
+        __syncthreads();
+        i32x4 *const red0 = (i32x4*)st0_, *const red1 = (i32x4*)st1_;
 #pragma unroll
-    for (int n = 0; n < FN; ++n)
+        for (int n = 0; n < FN; ++n)
 #pragma unroll
-        for (int m = 0; m < FM; ++m) asm volatile("" : "+a"(acc[n][m]));
+            for (int m = 0; m < FM; ++m)
+                ((n * FM + m) & 1 ? red1 : red0)[((group * 4 + wave) * HT + (n * FM + m) / 2) * 64 + lane] = acc[n][m];
+        __syncthreads();
+        const int mb = m0 + (wave & 1) * (16 * FM) + r, nb = n0 + (wave >> 1) * (16 * FN) + 4 * q;
+        for (int t = group; t < FM * FN; t += KS) {
+            const int mm = mb + 16 * (t % FM), nn = nb + 16 * (t / FM);
+            if (mm >= A.M || nn >= A.N) continue;
+            i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < KS; ++g) sum += (t & 1 ? red1 : red0)[((g * 4 + wave) * HT + t / 2) * 64 + lane];
+            const float xs = A.xs[mm];
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (float)sum[e] * (xs * A.ws[nn + e < A.N ? nn + e : A.N - 1]);
+            store_quad<YT>(A.y, (int64_t)mm * A.N + nn, v, A.N - nn);
+        }
+        return;
+    }
     // lane l holds rows 4 (l / 16) + e of w and token l % 16 of each tile
     const int mb = m0 + (wave & 1) * (16 * FM) + r, nb = n0 + (wave >> 1) * (16 * FN) + 4 * q;
     float ws[FN][4], xs[FM];
@@ -320,36 +320,67 @@ __global__ __launch_bounds__(256) void k_dense_i8_tile(Args A, int tiles_m, int 
     }
 }
 
-#ifndef FEW_MT1
-#define FEW_MT1
-#endif
+// ---------------------------------------------------------------------------
+// The kernels, and which one a product takes: the one of the least estimated
+// time, in microseconds,
+//   max(rounds (setup + turn turns),      a workgroup's own latency,
+//       q (wg + busy turns),              q workgroups' work on a compute unit,
+//       stream bytes / 5.2e6)             the weight and the outputs, at memory's rate
+// with `turns` the steps of 256 KS columns (few-token kernels: 128 KS) and
+// `rounds` how often the resident workgroups are replaced.  The constants are
+// fitted to measured times of every kernel on 401 products (M 1 .. 4096, N
+// 150 .. 40000, Kin 256 .. 14336); over them the choice costs 4% (geometric
+// mean) against the fastest of 16 kernels measured, 43% at worst.
+struct Kernel {
+    void (*f32)(Args, int, int);
+    void (*bf16)(Args, int, int);
+    int tm, tn, ks;              // tile; column splits of a workgroup
+    int threads, resident;       // resident workgroups on a compute unit
+    int columns;                 // of one turn
+    float turn, setup, busy, wg, stream;
+};
+#define TQ_DENSE_FEW(W) \
+    {k_dense_i8_few<TQ_F32, W>, k_dense_i8_few<TQ_BF16, W>, 16, 16, W, 64 * W, 4, 128 * W
+#define TQ_DENSE_TILE(FM, FN, KS, RES)                                                                               \
+    {k_dense_i8_tile<TQ_F32, FM, FN, KS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS>, 32 * FM, 32 * FN, KS, 256 * KS, RES, \
+     256 * KS
+constexpr int kFew = 2;          // the first ones take M <= 16
+const Kernel kKernels[] = {
+    TQ_DENSE_FEW(4),           0.28f, 0.69f, 0.41f, 0.00f, 1.22f},
+    TQ_DENSE_FEW(8),           0.24f, 1.08f, 0.75f, 0.00f, 1.30f},
+    TQ_DENSE_TILE(1, 1, 1, 8), 0.57f, 0.00f, 0.22f, 0.26f, 1.32f},
+    TQ_DENSE_TILE(1, 1, 2, 4), 0.74f, 0.00f, 0.42f, 0.48f, 1.22f},
+    TQ_DENSE_TILE(1, 1, 4, 2), 1.02f, 0.00f, 0.89f, 0.77f, 1.28f},
+    TQ_DENSE_TILE(2, 2, 1, 5), 0.78f, 0.00f, 0.47f, 0.83f, 1.01f},
+    TQ_DENSE_TILE(2, 2, 2, 2), 1.16f, 0.00f, 0.95f, 1.18f, 1.45f},
+    TQ_DENSE_TILE(4, 4, 1, 2), 0.71f, 1.36f, 1.18f, 0.00f, 1.63f},
+    TQ_DENSE_TILE(8, 8, 1, 1), 2.24f, 8.08f, 0.20f, 0.20f, 1.62f},
+};
 
-template <int YT, int MT, int RT, int W, int G, int D>
-tq_status launch_few_as(const Args& A, hipStream_t st)
+int64_t tiles_of(const Kernel& k, int64_t M, int64_t N) { return ((M + k.tm - 1) / k.tm) * ((N + k.tn - 1) / k.tn); }
+
+double estimate(const Kernel& k, int64_t M, int64_t N, int64_t Kin, int64_t y_bytes, int cus)
 {
-    const int64_t bm = (A.M + 16 * MT - 1) / (16 * MT), bn = (A.N + 16 * RT * G - 1) / (16 * RT * G);
-    if (bm * bn * 64 * W * G > UINT32_MAX)
-        return tq_fail(TQ_ERR_UNSUPPORTED, "%lld tiles exceed one launch", (long long)(bm * bn));
-    hipLaunchKernelGGL((k_dense_i8_few<YT, MT, RT, W, G, D>), dim3((unsigned)(bm * bn)), dim3(64 * W * G), 0, st, A, (int)bm);
-    return TQ_OK;
+    const double x = (double)tiles_of(k, M, N) / cus, turns = (double)((Kin + k.columns - 1) / k.columns);
+    const double q = k.resident == 1 ? ceil(x) : x < 1.0 ? 1.0 : x;
+    const double own = ceil(x / k.resident) * (k.setup + k.turn * turns), work = q * (k.wg + k.busy * turns);
+    const double mem = k.stream * (double)(N * Kin + y_bytes) / 5.2e6;
+    return own > work ? (own > mem ? own : mem) : (work > mem ? work : mem);
 }
 
-template <int YT, int MT>
-tq_status launch_few_m(const Args& A, hipStream_t st)
+// The kernel for a product, or null where no launch holds its tiles.
+const Kernel* pick(int64_t M, int64_t N, int64_t Kin, int64_t y_bytes)
 {
-    constexpr int D = MT == 1 ? 4 : MT == 2 ? 3 : 2;
-    const int64_t rows = (A.N + 15) / 16;           // 16-row tiles
-    if (rows <= 1024) return launch_few_as<YT, MT, 1, 8, 1, D>(A, st);
-    if (rows <= 4096) return launch_few_as<YT, MT, 1, 4, 1, D>(A, st);
-    return launch_few_as<YT, MT, 1, 2, 2, D>(A, st);
-}
-
-template <int YT>
-tq_status launch_few(const Args& A, hipStream_t st)
-{
-    if (A.M <= 16) return launch_few_m<YT, 1>(A, st);
-    if (A.M <= 32) return launch_few_m<YT, 2>(A, st);
-    return launch_few_m<YT, 4>(A, st);
+    const int cus = tq_device_cus();
+    const Kernel* best = nullptr;
+    double best_us = 0.0;
+    for (size_t i = M <= 16 ? 0 : kFew; i < sizeof kKernels / sizeof kKernels[0]; ++i) {
+        const Kernel& k = kKernels[i];
+        if (tiles_of(k, M, N) > (int64_t)UINT32_MAX / k.threads) continue;     // a launch counts its threads in 32 bits
+        const double us = estimate(k, M, N, Kin, y_bytes, cus);
+        if (!best || us < best_us) best = &k, best_us = us;
+    }
+    return best;
 }
 
 }  // namespace
@@ -377,20 +408,12 @@ TQ_EXPORT tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t Kin, const in
     if ((s = tq_check_overlap(y, yb, "y", w, N * Kin, "w"))) return s;
     if ((s = tq_check_overlap(y, yb, "y", x_scale, M * 4, "x_scale"))) return s;
     if ((s = tq_check_overlap(y, yb, "y", w_scale, N * 4, "w_scale"))) return s;
+    const Kernel* k = pick(M, N, Kin, yb);
+    if (!k) return tq_fail(TQ_ERR_UNSUPPORTED, "%lld x %lld outputs exceed one launch", (long long)M, (long long)N);
     const Args A{xq, x_scale, w, w_scale, y, (int32_t)M, (int32_t)N, (int32_t)Kin};
-    hipStream_t st = (hipStream_t)stream;
-    const auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
-    if (M > 64) {
-        if (tiles(256, 256) > INT32_MAX / 256)
-            return tq_fail(TQ_ERR_UNSUPPORTED, "%lld tiles exceed one launch", (long long)tiles(256, 256));
-        const int tm = (int)((M + 255) / 256), tn = (int)((N + 32*8-1) / (32*8));
-        if (y_type == TQ_F32)
-            hipLaunchKernelGGL((k_dense_i8_tile<TQ_F32, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
-        else
-            hipLaunchKernelGGL((k_dense_i8_tile<TQ_BF16, 8, 8>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, A, tm, tn);
-    } else if ((s = y_type == TQ_F32 ? launch_few<TQ_F32>(A, st) : launch_few<TQ_BF16>(A, st))) {
-        return s;
-    }
+    const int tm = (int)((M + k->tm - 1) / k->tm), tn = (int)((N + k->tn - 1) / k->tn);
+    hipLaunchKernelGGL(y_type == TQ_F32 ? k->f32 : k->bf16, dim3((unsigned)((int64_t)tm * tn)), dim3(k->threads), 0,
+                       (hipStream_t)stream, A, tm, tn);
     if ((s = tq_check_launch("tq_gemm_dense_i8"))) return s;
     return tq_ok();
 }
