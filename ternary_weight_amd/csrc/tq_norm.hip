@@ -7,10 +7,12 @@
 // Two reductions per row (the sum of squares, then max|n|, which needs r)
 // stand between reading x and writing y, so the row stays in registers
 // between them: a thread keeps V units of U consecutive elements, and the
-// row is read once.  The sum of squares is fp64 (an fp64 fma per element is
-// far below the memory time), rounded once to fp32; every other step is one
-// IEEE fp32 operation (this file is built with -ffp-contract=off), so the
-// int8 codes equal tq_act_quant_int8's of the same n, bit for bit.
+// row is read once, so memory bounds it (16381 x 4096, bf16 throughout with
+// the residual: 89.8 us, 5.98 TB/s, where a copy of 1 GiB reaches 5.15).
+// The sum of squares is fp64 (an fp64 fma per element is far below the memory
+// time), rounded once to fp32; every other step is one IEEE fp32 operation
+// (this file is built with -ffp-contract=off), so the int8 codes equal
+// tq_act_quant_int8's of the same n, bit for bit.
 #include <math.h>
 
 #include "tq_internal.h"
@@ -35,13 +37,37 @@ struct Args {
     float eps;
 };
 
-template <int XT>
-__device__ __forceinline__ f32x4 load4(const void* row, int i)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// U consecutive elements (a unit) as fp32, and back: 16 bytes per load or
+// store where the type allows (U = 8 for bf16, 4 for fp32).  Outputs are
+// stored non-temporally (2048 x 2560, residual, int8: 16.6 -> 11.9 us;
+// 16381 x 4096 bf16: 93.8 -> 89.8 us), inputs are not loaded so (10% slower).
+template <int TYPE, int U>
+__device__ __forceinline__ void load_u(const void* row, int i, float (&v)[U])
 {
-    if (XT == TQ_F32) return reinterpret_cast<const f32x4*>(row)[i];
-    const u32x2 v = reinterpret_cast<const u32x2*>(row)[i];
-    return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                 __uint_as_float(v.y & 0xFFFF0000u)};
+    if (TYPE == TQ_F32) {
+#pragma unroll
+        for (int k = 0; k < U / 4; ++k) {
+            const f32x4 f = reinterpret_cast<const f32x4*>(row)[i * (U / 4) + k];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * k + e] = f[e];
+        }
+    } else {
+        uint32_t w[U / 2];
+        if constexpr (U == 8) {
+            const u32x4 q = reinterpret_cast<const u32x4*>(row)[i];
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            const u32x2 q = reinterpret_cast<const u32x2*>(row)[i];
+            w[0] = q.x, w[1] = q.y;
+        }
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
@@ -50,13 +76,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-template <int YT>
-__device__ __forceinline__ void store4(void* row, int i, f32x4 v)
+template <int TYPE, int U>
+__device__ __forceinline__ void store_u(void* row, int i, const float (&v)[U])
 {
-    if (YT == TQ_F32)
-        reinterpret_cast<f32x4*>(row)[i] = v;
-    else
-        reinterpret_cast<u32x2*>(row)[i] = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+    if constexpr (TYPE == TQ_F32) {
+#pragma unroll
+        for (int k = 0; k < U / 4; ++k)
+            __builtin_nontemporal_store(f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]},
+                                        &reinterpret_cast<f32x4*>(row)[i * (U / 4) + k]);
+    } else if constexpr (U == 8) {
+        __builtin_nontemporal_store(u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                                          bf16_pair(v[6], v[7])},
+                                    &reinterpret_cast<u32x4*>(row)[i]);
+    } else {
+        __builtin_nontemporal_store(u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])},
+                                    &reinterpret_cast<u32x2*>(row)[i]);
+    }
 }
 
 __device__ __forceinline__ uint32_t quant1(float v, float inv)
@@ -79,36 +114,47 @@ __device__ __forceinline__ float wave_max(float v)
     return v;
 }
 
-// One row per workgroup of T threads, V units of 4 elements per thread.
+// One row per workgroup of T threads, V units of U elements per thread; the
+// weight stays in registers over the workgroup's rows.
 // Two reductions use two LDS arrays: a wave writes the first again only
 // after the second's barrier, which every wave reaches after reading the
 // first, so the loop over rows needs no further barrier.
-template <int XT, int RT, int YT, int T, int V>
+template <int XT, int RT, int YT, int U, int T, int V>
 __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
 {
     constexpr int W = T / 64;
     __shared__ double red_s[W];
     __shared__ float red_a[W];
-    const int tid = threadIdx.x, n4 = A.Kin >> 2;
+    const int tid = threadIdx.x, nu = A.Kin / U;
+    float w[V][U];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (tid + j * T < nu) load_u<TQ_F32, U>(A.w, tid + j * T, w[j]);
     for (int64_t m = blockIdx.x; m < A.M; m += gridDim.x) {
         const int64_t at = m * A.Kin;
         const uint8_t* xr = (const uint8_t*)A.x + at * (XT == TQ_F32 ? 4 : 2);
         const uint8_t* rr = RT == kNone ? nullptr : (const uint8_t*)A.res + at * (RT == TQ_F32 ? 4 : 2);
-        f32x4 h[V];
-        double s = 0.0;
+        float h[V][U];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = tid + j * T;
-            h[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (i < n4) {
-                h[j] = load4<XT>(xr, i);
-                if (RT != kNone) h[j] += load4<RT>(rr, i);
-            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) h[j][e] = 0.0f;
+            if (tid + j * T < nu) load_u<XT, U>(xr, tid + j * T, h[j]);
         }
+        if constexpr (RT != kNone)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (tid + j * T < nu) {
+                    float r[U];
+                    load_u<RT, U>(rr, tid + j * T, r);
+#pragma unroll
+                    for (int e = 0; e < U; ++e) h[j][e] += r[e];
+                }
+        double s = 0.0;
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s = fma((double)h[j][e], (double)h[j][e], s);
+            for (int e = 0; e < U; ++e) s = fma((double)h[j][e], (double)h[j][e], s);
         s = wave_sum(s);
         if (W > 1) {
             if ((tid & 63) == 0) red_s[tid >> 6] = s;
@@ -117,30 +163,29 @@ __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
 #pragma unroll
             for (int k = 0; k < W; ++k) s += red_s[k];
         }
-        if (RT != kNone && A.res_out) {
-            uint8_t* ro = (uint8_t*)A.res_out + at * (RT == TQ_F32 ? 4 : 2);
+        if constexpr (RT != kNone)
+            if (A.res_out) {
+                uint8_t* ro = (uint8_t*)A.res_out + at * (RT == TQ_F32 ? 4 : 2);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (tid + j * T < n4) store4<RT>(ro, tid + j * T, h[j]);
-        }
+                for (int j = 0; j < V; ++j)
+                    if (tid + j * T < nu) store_u<RT, U>(ro, tid + j * T, h[j]);
+            }
         const float mean = (float)(s / (double)A.Kin);
         const float r = 1.0f / sqrtf(mean + A.eps);
         float a = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = tid + j * T;
-            if (i < n4) {
-                const f32x4 w = reinterpret_cast<const f32x4*>(A.w)[i];
+        for (int j = 0; j < V; ++j)
+            if (tid + j * T < nu) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[j][e] = (h[j][e] * r) * w[e];
+                for (int e = 0; e < U; ++e) h[j][e] = (h[j][e] * r) * w[j][e];
+                if constexpr (YT != TQ_I8) {
+                    store_u<YT, U>((uint8_t*)A.y + at * (YT == TQ_F32 ? 4 : 2), tid + j * T, h[j]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < U; ++e) a = fmaxf(a, fabsf(h[j][e]));
+                }
             }
-            if (YT == TQ_I8) {
-                a = fmaxf(a, fmaxf(fmaxf(fabsf(h[j].x), fabsf(h[j].y)), fmaxf(fabsf(h[j].z), fabsf(h[j].w))));
-            } else if (i < n4) {
-                store4<YT>((uint8_t*)A.y + at * (YT == TQ_F32 ? 4 : 2), i, h[j]);
-            }
-        }
-        if (YT == TQ_I8) {
+        if constexpr (YT == TQ_I8) {
             a = wave_max(a);
             if (W > 1) {
                 if ((tid & 63) == 0) red_a[tid >> 6] = a;
@@ -153,9 +198,16 @@ __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
             uint32_t* q = (uint32_t*)((uint8_t*)A.y + at);
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (tid + j * T < n4)
-                    q[tid + j * T] = quant1(h[j].x, inv) | (quant1(h[j].y, inv) << 8) | (quant1(h[j].z, inv) << 16) |
-                                     (quant1(h[j].w, inv) << 24);
+                if (tid + j * T < nu) {
+                    uint32_t c[U / 4];
+#pragma unroll
+                    for (int k = 0; k < U / 4; ++k)
+                        c[k] = quant1(h[j][4 * k], inv) | (quant1(h[j][4 * k + 1], inv) << 8) |
+                               (quant1(h[j][4 * k + 2], inv) << 16) | (quant1(h[j][4 * k + 3], inv) << 24);
+                    if constexpr (U == 8)
+                        __builtin_nontemporal_store(u32x2{c[0], c[1]}, &reinterpret_cast<u32x2*>(q)[tid + j * T]);
+                    else __builtin_nontemporal_store(c[0], &q[tid + j * T]);
+                }
             if (tid == 0) A.ys[m] = a > 0.0f ? a / 127.0f : 0.0f;
         } else if (W > 1) {
             __syncthreads();   // red_s is read before the next row writes it
@@ -163,18 +215,33 @@ __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
     }
 }
 
+template <int XT, int RT, int YT, int U, int T, int V>
+void launch_as(const Args& A, hipStream_t st)
+{
+    const unsigned grid = (unsigned)(A.M < kMaxGrid ? A.M : kMaxGrid);
+    hipLaunchKernelGGL((k_rmsnorm<XT, RT, YT, U, T, V>), dim3(grid), dim3(T), 0, st, A);
+}
+
+// The threads of a row: as few as hold it in registers (fewer, fuller
+// workgroups hide each other's reductions; 2048 x 6912 fp32 to int8 with 256
+// threads of 8 units 16.6 us, with 1024 threads of 2 to 4 units 30 us).
 template <int XT, int RT, int YT>
 void launch(const Args& A, hipStream_t st)
 {
-    const unsigned grid = (unsigned)(A.M < kMaxGrid ? A.M : kMaxGrid);
-    if (A.Kin <= 1024)
-        hipLaunchKernelGGL((k_rmsnorm<XT, RT, YT, 64, 4>), dim3(grid), dim3(64), 0, st, A);
-    else if (A.Kin <= 4096)
-        hipLaunchKernelGGL((k_rmsnorm<XT, RT, YT, 256, 4>), dim3(grid), dim3(256), 0, st, A);
-    else if (A.Kin <= 16384)
-        hipLaunchKernelGGL((k_rmsnorm<XT, RT, YT, 1024, 4>), dim3(grid), dim3(1024), 0, st, A);
-    else
-        hipLaunchKernelGGL((k_rmsnorm<XT, RT, YT, 1024, 16>), dim3(grid), dim3(1024), 0, st, A);
+    // 8 elements per unit where x and the residual are bf16
+    if constexpr (XT == TQ_BF16 && RT != TQ_F32) {
+        if (A.Kin <= 1024) launch_as<XT, RT, YT, 8, 64, 2>(A, st);
+        else if (A.Kin <= 4096) launch_as<XT, RT, YT, 8, 256, 2>(A, st);
+        else if (A.Kin <= 8192) launch_as<XT, RT, YT, 8, 256, 4>(A, st);
+        else if (A.Kin <= 16384) launch_as<XT, RT, YT, 8, 512, 4>(A, st);
+        else launch_as<XT, RT, YT, 8, 1024, 8>(A, st);
+    } else {
+        if (A.Kin <= 1024) launch_as<XT, RT, YT, 4, 64, 4>(A, st);
+        else if (A.Kin <= 4096) launch_as<XT, RT, YT, 4, 256, 4>(A, st);
+        else if (A.Kin <= 8192) launch_as<XT, RT, YT, 4, 256, 8>(A, st);
+        else if (A.Kin <= 16384) launch_as<XT, RT, YT, 4, 512, 8>(A, st);
+        else launch_as<XT, RT, YT, 4, 1024, 16>(A, st);
+    }
 }
 
 template <int XT, int RT>

@@ -65,7 +65,7 @@ def test_dispatch_refusals():
     assert dispatch(width=16, x=E, xs=E) == tq.ERR_ARG and dispatch(offs=C + 8) == tq.ERR_ARG
     need = tq.moe_dispatch_workspace_size(10000, 2, 4)
     assert need > 0 and tq.moe_dispatch_workspace_size(64, 8, 128) == 0
-    assert tq.moe_dispatch_workspace_size(1, 1, 1024) > 0
+    assert tq.moe_dispatch_workspace_size(1, 1, 1024) == 0 and tq.moe_dispatch_workspace_size(1025, 1, 1024) > 0
     assert dispatch(T=10000) == tq.ERR_ARG and dispatch(T=10000, ws=E, nws=need - 1) == tq.ERR_ARG
     assert dispatch(T=10000, ws=E + 4, nws=need) == tq.ERR_ALIGN and dispatch(T=10000, ws=A, nws=need) == tq.ERR_ARG
     with pytest.raises(tq.TQError) as e:
