@@ -101,6 +101,31 @@ def test_large(M, N, K, yt):
     assert torch.equal(y, want.to(y.dtype))
 
 
+# Products of the middle sizes and of the large ones that the wider tiles take, none of whose edges is whole: tokens,
+# outputs and columns of every remainder of a tile (Kin mod 256: 16 .. 240, and 0)
+EDGES = [(700, 1001, 3312), (300, 4097, 2320), (200, 5002, 4448), (300, 2563, 1856), (257, 7001, 2016), (513, 4097, 896),
+         (700, 5002, 304), (2050, 4097, 3584), (1500, 9999, 752), (1025, 9999, 1280), (1500, 7001, 3808), (1025, 9999, 3152),
+         (1500, 9999, 1568), (1025, 12001, 4480), (1281, 10001, 1152), (1300, 10002, 1040), (1537, 9001, 1936),
+         (257, 2049, 2720), (70, 5002, 704), (130, 1001, 2672), (1023, 9985, 16), (1025, 9987, 176)]
+
+
+@pytest.mark.parametrize("M,N,K", EDGES)
+def test_tiles_with_edges(M, N, K):
+    from ternary_weight_amd import tq
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(K)
+    xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs, ws = torch.rand(M, device="cuda", generator=g), torch.rand(N, device="cuda", generator=g) - 0.5
+    want = (xq.double() @ wq.double().t()).float() * (xs[:, None] * ws[None, :])
+    for yt, dt in ((F32, torch.float32), (BF16, torch.bfloat16)):
+        whole = torch.full((64 + M * N + 4096,), 99.0, dtype=dt, device="cuda")
+        print("edges", M, N, K, yt, flush=True)
+        tq.gemm_dense_i8(M, N, K, xq, xs, wq, ws, yt, whole[64:64 + M * N])
+        assert torch.equal(whole[64:64 + M * N].view(M, N), want.to(dt))
+        assert torch.all(whole[:64] == 99.0) and torch.all(whole[64 + M * N:] == 99.0)
+
+
 def test_weight_beyond_32_bit_offsets():
     """A weight of more than 4 GiB: its last rows."""
     from ternary_weight_amd import tq
