@@ -35,6 +35,7 @@
  *    the library keeps no reference after the call's work has run and
  *    allocates no device memory (tq_ternarize_noalloc's fixed scratch array
  *    aside, see there).
+ *  - Arrays and `stream` belong to the calling thread's current device.
  *  - `stream` is a hipStream_t (NULL = the default stream).  Calls enqueue
  *    their kernels on it and return without waiting, except tq_pack (see
  *    there) and tq_gemv_grouped_prepare.
@@ -586,7 +587,7 @@ tq_status tq_moe_combine_grad(int64_t tokens, int32_t top_k, int64_t width, int6
  *   w        device int8 [N][Kin] row-major, every value -128 .. 127, 16-byte
  *            aligned, w_scale device fp32 [N]
  *   y        device [M][N] of y_type; must not overlap another array (TQ_ERR_ARG)
- * Kin is a multiple of 16 up to 65536 (0 gives y = 0 times the scales), N and M up to 2^24;
+ * Kin is a multiple of 16 up to 65536 (0: sums of nothing), N and M up to 2^24;
  * M = 0 or N = 0 is a no-op.
  */
 tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t in_features, const int8_t* xq, const float* x_scale,

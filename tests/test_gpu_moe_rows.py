@@ -73,8 +73,47 @@ def test_sort(T, k, E, kind):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
+@pytest.mark.parametrize("T,k,E", [(128, 8, 1024), (1024, 1, 960), (16, 64, 5), (1025, 1, 961), (300, 4, 1000), (256, 4, 3),
+                                   (257, 4, 3), (8193, 1, 2), (66000, 8, 1024)])
+def test_sort_at_its_kernels_edges(T, k, E, kind):
+    """Pair and expert counts on both sides of each way of sorting."""
+    test_sort(T, k, E, kind)
+
+
+def test_more_tokens_than_waves():
+    """Batches that a launch walks in a loop: rows there and back, and the gradient."""
+    from ternary_weight_amd import tq
+    torch = _torch()
+    T, E, H = (1 << 22) + 77, 3, 16
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.randint(-1, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randint(-127, 128, (T, H), generator=g, device="cuda", dtype=torch.int8)
+    xsc = torch.rand(T, device="cuda", generator=g)
+    rows, pairs, offs, xs, xss = dispatch(ids.cpu().numpy(), E, H, I8, x, xsc)
+    flat = ids.view(-1).long()
+    order = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    n = int((flat >= 0).sum())
+    assert int(offs[E]) == n and torch.equal(pairs[:n].long(), order[:n]) and torch.all(pairs[n:] == -1)
+    assert torch.equal(xs[:n], x[order[:n]]) and torch.equal(xss[:n], xsc[order[:n]]) and torch.all(xs[n:] == 7)
+    ys = torch.randn(T, H, device="cuda", generator=g)
+    w = torch.rand(T, 1, device="cuda", generator=g)
+    y = torch.empty(T, H, device="cuda")
+    tq.moe_combine(T, 1, H, T, rows, w, F32, ys, F32, y)
+    used = (flat >= 0)[:, None]
+    want = torch.where(used, ys[rows.view(-1).clamp_min(0).long()] * w, 0.0)       # one product: exact rounding
+    assert torch.equal(y, want)
+    d_ys, d_w = torch.full((T, H), 3.0, device="cuda"), torch.empty(T, 1, device="cuda")
+    tq.moe_combine_grad(T, 1, H, T, rows, w, F32, y, F32, ys, d_ys, d_w)
+    at = rows.view(-1)[flat >= 0].long()
+    assert torch.equal(d_ys[at], (y * w)[flat >= 0]) and torch.all(d_ys[n:] == 3.0)
+    dots = torch.where(used, (y.double() * ys[rows.view(-1).clamp_min(0).long()].double()).sum(1, keepdim=True), 0.0)
+    mag = torch.where(used, (y.double() * ys[rows.view(-1).clamp_min(0).long()].double()).abs().sum(1, keepdim=True), 0.0)
+    assert torch.all((d_w.double() - dots).abs() <= 32 * ref.U24 * mag)
+
+
 @pytest.mark.parametrize("xt", [F32, BF16, I8])
-@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 16), (5, 3, 4, 48), (64, 8, 128, 2048), (200, 2, 9, 4112),
+@pytest.mark.parametrize("T,k,E,H", [(300, 5, 9, 16400), (1, 1, 1, 16), (5, 3, 4, 48), (64, 8, 128, 2048), (200, 2, 9, 4112),
                                      (1500, 8, 33, 272), (7, 4, 6, 65536)])
 def test_rows(T, k, E, H, xt):
     torch = _torch()
