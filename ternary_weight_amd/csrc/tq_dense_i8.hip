@@ -116,15 +116,23 @@ __global__ __launch_bounds__(64 * W) void k_dense_i8_few(Args A, int tiles_m, in
 // that the 8 lanes of one LDS pass (rows R .. R + 7 of one chunk) fall in
 // distinct banks.  Loads go from memory straight to LDS: a wave's load fills
 // 1 KiB in lane order (8 rows), so the swizzle is applied to the address that
-// each lane reads.  Two stages alternate; while the matrix cores run on one
-// step's fragments those of the next are read from LDS.  At the second step
+// each lane reads.  While the matrix cores run on one step's fragments those of
+// the next are read from LDS.  At the second step
 // of a stage the waves meet: the next stage has then arrived, and every
 // fragment of this one is in registers, so its place takes the loads of the
 // stage after the next, spread over the step's MFMAs.
-// The first two stages are the last Kin % 256 columns (a whole 256 where that
-// is 0), their x fragments past Kin set to zero, so that the loop needs no
-// masks.  Rows past M and N are read as the last row (their outputs are not
-// stored).
+// The ring holds NS stages, NS - 1 of them requested ahead.  The columns are
+// walked from the end: the first stage may be short, its x fragments past Kin
+// are set to zero, and it starts at the place of the ring from which whole
+// turns are left, so that the loop needs no masks and no tests.  KS groups of
+// 4 waves share a tile's columns, a block of 128 each in turn, and add their
+// sums in LDS.  Rows past M and N are read as the last row (their outputs are
+// not stored).
+// 8192 x 14336 x 4096, bf16 out: 0.40 ms, 2.4 POP/s, the matrix cores busy 54%
+// of the time at the clock the power limit leaves (int8 MFMAs alone on random
+// values reach 3.2 to 3.9 POP/s, a library product of 8192^3 2.1 POP/s, this
+// one 2.6); LDS reads without bank conflicts; what is left over is the
+// epilogue, in which all tiles store at once.
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_u8* dst, uint32_t voff, uint32_t soff)
@@ -155,16 +163,21 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
     *tn = in / wide;
 }
 
-template <int YT, int FM, int FN, int KS>
+template <int YT, int FM, int FN, int KS, int NS>
 __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m, int tiles_n)
 {
     constexpr int TM = 32 * FM, TN = 32 * FN, XL = TM / 32, WL = TN / 32, NL = XL + WL;   // loads per wave and stage
     constexpr int STAGE = (TM + TN) * 128;
-    __shared__ __attribute__((aligned(1024))) uint8_t st0_[KS * STAGE], st1_[KS * STAGE];
+    static_assert(NS >= 2 && NS <= 4, "stages in the ring");
+    // an array per stage: the compiler then sees that a read of one does not wait for the loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t st0_[KS * STAGE], st1_[KS * STAGE], st2_[NS > 2 ? KS * STAGE : 16],
+        st3_[NS > 3 ? KS * STAGE : 16];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave_id & 3, group = wave_id >> 2;
     uint8_t* const st0 = st0_ + group * STAGE;
     uint8_t* const st1 = st1_ + group * STAGE;
+    uint8_t* const st2 = NS > 2 ? st2_ + group * STAGE : st2_;
+    uint8_t* const st3 = NS > 3 ? st3_ + group * STAGE : st3_;
     int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
     const int m0 = tm * TM, n0 = tn * TN, K = A.Kin;
@@ -178,14 +191,22 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
         const int R = ((l < XL ? l : l - XL) * 4 + wave) * 8 + (lane >> 3), rows = l < XL ? mrows : nrows;
-        vo[l] = (uint32_t)(R < rows ? R : rows - 1) * (uint32_t)K;
+        vo[l] = (uint32_t)(R < rows ? R : rows - 1) * (uint32_t)K + 16 * c;
     }
-    // the wave's loads l0 .. l1 - 1 of the stage at column `col`; lanes add `off` (their chunk's offset)
-    auto request = [&](uint8_t* st, uint32_t col, uint32_t off, int l0, int l1) __attribute__((always_inline)) {
+    // Stage j of this group is the block of 128 columns (stages - 1 - j) * KS + group: stage 0 holds the last columns,
+    // `valid` of them (none where the block is past Kin)
+    const int blocks = (K + 127) >> 7, stages = (blocks + KS - 1) / KS;
+    const int last = ((stages - 1) * KS + group) * 128, valid = K - last < 0 ? 0 : K - last < 128 ? K - last : 128;
+    // The wave's loads l0 .. l1 - 1 of stage j, lanes moved back by `back`.  Past the last stage loads keep the count:
+    // of the tile's first columns, or, with more of them, all of one address.
+    auto request = [&](uint8_t* st, int j, uint32_t back, int l0, int l1) __attribute__((always_inline)) {
+        const bool live = j < stages;
+        const uint32_t col = live ? last - j * KS * 128 : 0;
 #pragma unroll
         for (int l = l0; l < l1; ++l) {
             const int id = (l < XL ? l : l - XL) * 4 + wave;
-            load_lds16(l < XL ? rx : rw, (lds_u8*)st + (l < XL ? 0 : TM * 128) + id * 1024, vo[l] + off, col);
+            load_lds16(l < XL ? rx : rw, (lds_u8*)st + (l < XL ? 0 : TM * 128) + id * 1024,
+                       NS == 2 || live ? vo[l] - back : 0, col);
         }
     };
     const int at0 = r * 128 + 16 * (q ^ (r & 7)), at1 = at0 ^ 64;      // chunks q and 4 + q of the lane's row
@@ -196,20 +217,22 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
 #pragma unroll
         for (int m = 0; m < FM; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
     i32x4 fx0[FM], fw0[FN], fx1[FM], fw1[FN];
-    // one step on fragments (x, w); those of the next come from `next` + at.  LOAD: the second step of a stage: the
-    // stage at column `col` is requested into `free`, the place of the step's own
-    auto step = [&](bool load, i32x4 (&x)[FM], i32x4 (&w)[FN], const uint8_t* next, int at, i32x4 (&xn)[FM],
-                    i32x4 (&wn)[FN], uint8_t* free, uint32_t col, uint32_t off) __attribute__((always_inline)) {
-        if (load) {
-            __builtin_amdgcn_s_waitcnt(0x0070);       // vmcnt(0): the next stage's loads; lgkmcnt(0): this one's reads
+    // One step: MFMAs on (x, w) while the fragments (xn, wn) are read from `next` + at.  The second step of a stage
+    // begins with the meeting and requests stage `j` into `free`, the stage's own place.
+    // A row of MFMAs covers the reads of one x and one w fragment and, spread, a load or two: all of a step's loads at
+    // once hold the wave at their issue while its matrix core idles (4096 x 4096 x 4096: 3 per row 59.8, 4 per row
+    // 65.8 us, against 55.9).
+    auto step = [&](bool second, const i32x4 (&x)[FM], const i32x4 (&w)[FN], const uint8_t* next, int at, i32x4 (&xn)[FM],
+                    i32x4 (&wn)[FN], uint8_t* free, int j) __attribute__((always_inline)) {
+        if (second) {
+            wait_vm<(NS - 2) * NL>();                     // the next stage's loads have arrived ..
+            __builtin_amdgcn_s_waitcnt(0xC07F);           // .. and lgkmcnt(0): this one's reads are done
             __builtin_amdgcn_s_barrier();
         }
         __builtin_amdgcn_sched_barrier(0);
-        // a row of MFMAs covers the reads of one x and one w fragment and, spread, a load or two: all of a step's
-        // loads at once hold the wave at their issue while its matrix core idles
 #pragma unroll
         for (int n = 0; n < FN; ++n) {
-            if (load) request(free, col, off, n * NL / FN, (n + 1) * NL / FN);
+            if (second) request(free, j, 0, n * NL / FN, (n + 1) * NL / FN);
             wn[n] = *(const i32x4*)(next + bw + at + n * 2048);
 #pragma unroll
             for (int m = n * FM / FN; m < (n + 1) * FM / FN; ++m) xn[m] = *(const i32x4*)(next + bx + at + m * 2048);
@@ -219,43 +242,58 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    // both steps of the stage in `cur`, `next` the one after it; stage j + NS is requested
+    auto stage = [&](uint8_t* cur, const uint8_t* next, int j) __attribute__((always_inline)) {
+        step(false, fx0, fw0, cur, at1, fx1, fw1, nullptr, 0);
+        step(true, fx1, fw1, next, at0, fx0, fw0, cur, j + NS);
+    };
     auto mask = [&](i32x4 (&x)[FM], int left) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < FM; ++m) x[m] = 16 * q < left ? x[m] : i32x4{0, 0, 0, 0};
     };
+    // a stage of the first turn: begins with the first stage's fragments, and masks its columns past Kin
+    auto masked = [&](int place, int skip, uint8_t* cur, const uint8_t* next) __attribute__((always_inline)) {
+        if (place < NS - 1 && place < skip) return;      // skip < NS
+        const int j = place - skip, left = j == 0 ? valid : 128;
+        if (j == 0) {
+            wait_vm<(NS - 1) * NL>();
+            __builtin_amdgcn_s_barrier();
+#pragma unroll
+            for (int n = 0; n < FN; ++n) fw0[n] = *(const i32x4*)(cur + bw + at0 + n * 2048);
+#pragma unroll
+            for (int m = 0; m < FM; ++m) fx0[m] = *(const i32x4*)(cur + bx + at0 + m * 2048);
+        }
+        mask(fx0, left);
+        step(false, fx0, fw0, cur, at1, fx1, fw1, nullptr, 0);
+        mask(fx1, left - 64);
+        step(true, fx1, fw1, next, at0, fx0, fw0, cur, j + NS);
+    };
     if (K > 0) {
-        // 256 columns at a time, dealt to the groups in turn from the end: `first` may be short, or past Kin and empty
-        const int chunks = (K + 255) >> 8, turns = (chunks + KS - 1) / KS;
-        const int first = ((turns - 1) * KS + group) * 256, tail = K - first < 0 ? 0 : K - first < 256 ? K - first : 256;
-        const int left1 = tail > 128 ? tail - 128 : 0;
-        // chunks past Kin are read from column 0
-        const uint32_t off = 16 * c, offt0 = 16 * c < tail ? first + 16 * c : 0, offt1 = 16 * c < left1 ? first + 128 + 16 * c : 0;
-        request(st0, 0, offt0, 0, NL);
-        request(st1, 0, offt1, 0, NL);
-        wait_vm<NL>();
-        __builtin_amdgcn_s_barrier();
-#pragma unroll
-        for (int n = 0; n < FN; ++n) fw0[n] = *(const i32x4*)(st0 + bw + at0 + n * 2048);
-#pragma unroll
-        for (int m = 0; m < FM; ++m) fx0[m] = *(const i32x4*)(st0 + bx + at0 + m * 2048);
-        // the four steps of `first`; a stage past the group's last is requested again from column 0
-        const bool more = turns > 1;
-        const uint32_t off1 = more ? off : 0;
-        int k = more ? first - KS * 256 : 0;
-        mask(fx0, tail);
-        step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
-        mask(fx1, tail - 64);
-        step(true, fx1, fw1, st1, at0, fx0, fw0, st0, k, off1);
-        mask(fx0, left1);
-        step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
-        mask(fx1, left1 - 64);
-        step(true, fx1, fw1, st0, at0, fx0, fw0, st1, k + (more ? 128 : 0), off1);
-        for (int i = 1; i < turns; ++i) {
-            k = k >= KS * 256 ? k - KS * 256 : 0;
-            step(false, fx0, fw0, st0, at1, fx1, fw1, nullptr, 0, 0);
-            step(true, fx1, fw1, st1, at0, fx0, fw0, st0, k, off);
-            step(false, fx0, fw0, st1, at1, fx1, fw1, nullptr, 0, 0);
-            step(true, fx1, fw1, st0, at0, fx0, fw0, st1, k + 128, off);
+        // turns of NS stages; the first may be short: it starts at place `skip` of the ring
+        const int turns = (stages + NS - 1) / NS, skip = turns * NS - stages;
+        // the first NS stages, in their order: loads return in it
+        auto begin = [&](int place, uint8_t* st, bool wrapped) __attribute__((always_inline)) {
+            if ((place < skip) != wrapped) return;
+            // columns past Kin in the last block are read from its first chunk, a block past Kin is the one before it
+            const bool first = !wrapped && place == skip, none = first && valid == 0;
+            request(st, none ? 1 : place - skip + (wrapped ? NS : 0), first && !none && 16 * c >= valid ? 16 * c : 0, 0, NL);
+        };
+        begin(0, st0, false);
+        begin(1, st1, false);
+        if constexpr (NS > 2) begin(2, st2, false);
+        if constexpr (NS > 3) begin(3, st3, false);
+        begin(0, st0, true);
+        if constexpr (NS > 2) begin(1, st1, true);
+        if constexpr (NS > 3) begin(2, st2, true);
+        masked(0, skip, st0, st1);
+        masked(1, skip, st1, NS > 2 ? st2 : st0);
+        if constexpr (NS > 2) masked(2, skip, st2, NS > 3 ? st3 : st0);
+        if constexpr (NS > 3) masked(3, skip, st3, st0);
+        for (int j = NS - skip; j < stages; j += NS) {
+            stage(st0, st1, j);
+            stage(st1, NS > 2 ? st2 : st0, j + 1);
+            if constexpr (NS > 2) stage(st2, NS > 3 ? st3 : st0, j + 2);
+            if constexpr (NS > 3) stage(st3, st0, j + 3);
         }
         wait_vm<0>();     // the requests past the last stage: no load may land after the workgroup has left
     }
@@ -322,50 +360,51 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
 
 // ---------------------------------------------------------------------------
 // The kernels, and which one a product takes: the one of the least estimated
-// time, in microseconds,
-//   max(rounds (setup + turn turns),      a workgroup's own latency,
-//       q (wg + busy turns),              q workgroups' work on a compute unit,
-//       stream bytes / 5.2e6)             the weight and the outputs, at memory's rate
-// with `turns` the steps of 256 KS columns (few-token kernels: 128 KS) and
-// `rounds` how often the resident workgroups are replaced.  The constants are
-// fitted to measured times of every kernel on 401 products (M 1 .. 4096, N
-// 150 .. 40000, Kin 256 .. 14336); over them the choice costs 4% (geometric
-// mean) against the fastest of 16 kernels measured, 43% at worst.
+// time, in microseconds: `base` and a smooth maximum (the 8th root of the sum
+// of 8th powers) of
+//   rounds (setup + turn turns)     a workgroup's own latency,
+//   q (wg + busy turns)             q workgroups' work on a compute unit,
+//   stream bytes / 5.2e6            the operands and outputs, at memory's rate,
+// with `turns` the 128-column blocks of one column group, `rounds` how often
+// the resident workgroups are replaced and q the tiles per compute unit.  The
+// constants are fitted to measured times of every kernel on 401 products (M 1
+// .. 4096, N 150 .. 40000, Kin 256 .. 14336, fp32 outputs); over them the
+// choice costs 3.3% (geometric mean) against the fastest of 24 kernels
+// measured, 47% at worst (160 x 12000 x 14336).
 struct Kernel {
     void (*f32)(Args, int, int);
     void (*bf16)(Args, int, int);
-    int tm, tn, ks;              // tile; column splits of a workgroup
-    int threads, resident;       // resident workgroups on a compute unit
-    int columns;                 // of one turn
-    float turn, setup, busy, wg, stream;
+    int tm, tn;                  // tile
+    int groups, threads;         // column groups of a workgroup
+    int resident;                // workgroups on a compute unit
+    double turn, setup, busy, wg, stream, base;
 };
-#define TQ_DENSE_FEW(W) \
-    {k_dense_i8_few<TQ_F32, W>, k_dense_i8_few<TQ_BF16, W>, 16, 16, W, 64 * W, 4, 128 * W
-#define TQ_DENSE_TILE(FM, FN, KS, RES)                                                                               \
-    {k_dense_i8_tile<TQ_F32, FM, FN, KS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS>, 32 * FM, 32 * FN, KS, 256 * KS, RES, \
-     256 * KS
-constexpr int kFew = 2;          // the first ones take M <= 16
+#define TQ_DENSE_FEW(W) {k_dense_i8_few<TQ_F32, W>, k_dense_i8_few<TQ_BF16, W>, 16, 16, W, 64 * W, 4
+#define TQ_DENSE_TILE(FM, FN, KS, NS, RES)                                                                           \
+    {k_dense_i8_tile<TQ_F32, FM, FN, KS, NS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS, NS>, 32 * FM, 32 * FN, KS, 256 * KS, \
+     RES
 const Kernel kKernels[] = {
-    TQ_DENSE_FEW(4),           0.28f, 0.69f, 0.41f, 0.00f, 1.22f},
-    TQ_DENSE_FEW(8),           0.24f, 1.08f, 0.75f, 0.00f, 1.30f},
-    TQ_DENSE_TILE(1, 1, 1, 8), 0.57f, 0.00f, 0.22f, 0.26f, 1.32f},
-    TQ_DENSE_TILE(1, 1, 2, 4), 0.74f, 0.00f, 0.42f, 0.48f, 1.22f},
-    TQ_DENSE_TILE(1, 1, 4, 2), 1.02f, 0.00f, 0.89f, 0.77f, 1.28f},
-    TQ_DENSE_TILE(2, 2, 1, 5), 0.78f, 0.00f, 0.47f, 0.83f, 1.01f},
-    TQ_DENSE_TILE(2, 2, 2, 2), 1.16f, 0.00f, 0.95f, 1.18f, 1.45f},
-    TQ_DENSE_TILE(4, 4, 1, 2), 0.71f, 1.36f, 1.18f, 0.00f, 1.63f},
-    TQ_DENSE_TILE(8, 8, 1, 1), 2.24f, 8.08f, 0.20f, 0.20f, 1.62f},
+    TQ_DENSE_FEW(4),              0.027, 1.153, 0.297, 0.000, 1.038, 2.994},     // M <= 16 only
+    TQ_DENSE_TILE(1, 1, 1, 4, 5), 0.000, 1.401, 0.114, 0.336, 0.968, 2.847},
+    TQ_DENSE_TILE(1, 1, 2, 4, 2), 0.000, 2.089, 0.180, 1.262, 1.061, 2.113},
+    TQ_DENSE_TILE(2, 2, 1, 3, 3), 0.000, 2.144, 0.232, 1.029, 1.116, 2.052},
+    TQ_DENSE_TILE(2, 2, 2, 4, 1), 0.411, 0.000, 0.326, 4.105, 1.159, 0.135},
+    TQ_DENSE_TILE(4, 4, 1, 3, 1), 0.450, 4.709, 0.014, 0.572, 1.739, 0.018},
+    TQ_DENSE_TILE(4, 8, 1, 3, 1), 0.796, 7.543, 0.226, 0.510, 1.211, 0.000},
+    TQ_DENSE_TILE(6, 8, 1, 2, 1), 0.204, 3.694, 1.123, 10.65, 1.489, 0.000},
+    TQ_DENSE_TILE(8, 8, 1, 2, 1), 0.254, 2.762, 1.331, 14.35, 1.456, 0.000},
 };
 
 int64_t tiles_of(const Kernel& k, int64_t M, int64_t N) { return ((M + k.tm - 1) / k.tm) * ((N + k.tn - 1) / k.tn); }
 
 double estimate(const Kernel& k, int64_t M, int64_t N, int64_t Kin, int64_t y_bytes, int cus)
 {
-    const double x = (double)tiles_of(k, M, N) / cus, turns = (double)((Kin + k.columns - 1) / k.columns);
+    const double x = (double)tiles_of(k, M, N) / cus;
+    const double turns = (double)(((Kin + 127) / 128 + k.groups - 1) / k.groups);
     const double q = k.resident == 1 ? ceil(x) : x < 1.0 ? 1.0 : x;
     const double own = ceil(x / k.resident) * (k.setup + k.turn * turns), work = q * (k.wg + k.busy * turns);
-    const double mem = k.stream * (double)(N * Kin + y_bytes) / 5.2e6;
-    return own > work ? (own > mem ? own : mem) : (work > mem ? work : mem);
+    const double mem = k.stream * (double)(N * Kin + M * Kin + y_bytes) / 5.2e6;
+    return k.base + pow(pow(own, 8.0) + pow(work, 8.0) + pow(mem, 8.0), 0.125);
 }
 
 // The kernel for a product, or null where no launch holds its tiles.
@@ -374,7 +413,7 @@ const Kernel* pick(int64_t M, int64_t N, int64_t Kin, int64_t y_bytes)
     const int cus = tq_device_cus();
     const Kernel* best = nullptr;
     double best_us = 0.0;
-    for (size_t i = M <= 16 ? 0 : kFew; i < sizeof kKernels / sizeof kKernels[0]; ++i) {
+    for (size_t i = M <= 16 ? 0 : 1; i < sizeof kKernels / sizeof kKernels[0]; ++i) {
         const Kernel& k = kKernels[i];
         if (tiles_of(k, M, N) > (int64_t)UINT32_MAX / k.threads) continue;     // a launch counts its threads in 32 bits
         const double us = estimate(k, M, N, Kin, y_bytes, cus);
