@@ -106,7 +106,10 @@ def test_large(M, N, K, yt):
 EDGES = [(700, 1001, 3312), (300, 4097, 2320), (200, 5002, 4448), (300, 2563, 1856), (257, 7001, 2016), (513, 4097, 896),
          (700, 5002, 304), (2050, 4097, 3584), (1500, 9999, 752), (1025, 9999, 1280), (1500, 7001, 3808), (1025, 9999, 3152),
          (1500, 9999, 1568), (1025, 12001, 4480), (1281, 10001, 1152), (1300, 10002, 1040), (1537, 9001, 1936),
-         (257, 2049, 2720), (70, 5002, 704), (130, 1001, 2672), (1023, 9985, 16), (1025, 9987, 176)]
+         (257, 2049, 2720), (70, 5002, 704), (130, 1001, 2672), (1023, 9985, 16), (1025, 9987, 176),
+         (200, 30001, 960), (385, 9999, 2128), (450, 12001, 1616), (1025, 7001, 1568), (2050, 2563, 496), (70, 7001, 6816),
+         (200, 2563, 7280), (450, 1001, 7504), (130, 4097, 3040), (200, 9999, 2576), (257, 7001, 4000), (700, 4097, 1520),
+         (257, 30001, 4656), (700, 12001, 672)]
 
 
 @pytest.mark.parametrize("M,N,K", EDGES)
