@@ -1,4 +1,5 @@
-"""Build libtq.so (the HIP library) and libtqsynth.so (the input generator) for gfx950.
+"""Build libtq.so (the HIP library) and libtqsynth.so (the input generator) for gfx950,
+and _tqbind.so (the binding's native marshalling: host code against torch's headers).
 
 Each .hip source is compiled separately (in parallel) with hipcc and linked
 into a shared library next to its sources' package.  Run as
@@ -16,6 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBTQ = os.path.join(PKG, "libtq.so")
+BIND_SRC = os.path.join(CSRC, "tq_bind.cpp")
+LIBBIND = os.path.join(PKG, "_tqbind.so")
 SYNTH_SRC = os.path.join(ROOT, "synth", "synth_kernels.hip")
 LIBSYNTH = os.path.join(ROOT, "synth", "libtqsynth.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
@@ -93,8 +96,30 @@ def build_synth() -> str:
     return LIBSYNTH
 
 
+def build_bind() -> str:
+    if INCREMENTAL and os.path.exists(LIBBIND) and os.path.getmtime(LIBBIND) > max(
+            os.path.getmtime(BIND_SRC), os.path.getmtime(os.path.join(ROOT, "include", "tq.h"))):
+        return LIBBIND
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = LIBBIND + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           *["-isystem" + i for i in include_paths()], "-I" + sysconfig.get_paths()["include"], BIND_SRC,
+           "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (BIND_SRC, " ".join(cmd), r.stderr[-4000:]))
+    os.replace(tmp, LIBBIND)
+    return LIBBIND
+
+
 def build_all() -> None:
     build_libtq()
+    build_bind()
     if os.path.exists(SYNTH_SRC):
         build_synth()
 

@@ -149,55 +149,52 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_torch = _raw_stream = _kinds = None
+_torch = _raw_stream = None
 
 
 def _load_torch():
-    global _torch, _raw_stream, _kinds
+    global _torch, _raw_stream
     import torch
-    # bf16 arrays may come as 16-bit integers holding the bits
-    _kinds = {F32: (torch.float32,), BF16: (torch.bfloat16, torch.int16, torch.uint16), I8: (torch.int8,),
-              "i32": (torch.int32,)}
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 0.1 us, a Stream object takes 2.7
     _torch = torch
     return torch
 
 
+def _current_stream(device=None):
+    """Handle of torch's current stream."""
+    torch = _torch or _load_torch()
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        torch = _torch or _load_torch()
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _device():
-    """The current device's number; -2, which no tensor has, before the GPU is in use."""
-    cuda = (_torch or _load_torch()).cuda
-    return cuda.current_device() if cuda.is_initialized() else -2
+_native_module = None
 
 
-def _dense(t, name, kind, count, device):
-    """Device pointer of an array that a call reads or writes as `count`
-    consecutive elements.  Of a tensor it checks what the C call cannot see:
-    its type (kind: a tq_dtype, "i32" or "any"), layout, length and device."""
-    if t is None or isinstance(t, int):
-        return t
-    kinds = _kinds.get(kind)
-    if (kinds is None or t.dtype in kinds) and t.is_contiguous() and t.numel() >= count and t.get_device() == device:
-        return t.data_ptr()
-    if kinds is not None and t.dtype not in kinds:
-        raise ValueError("%s: %s, not %s" % (name, t.dtype, kinds[0]))
-    if not t.is_contiguous():
-        raise ValueError("%s: not contiguous (strides %s)" % (name, tuple(t.stride())))
-    if t.numel() < count:
-        raise ValueError("%s: %d elements, needs %d" % (name, t.numel(), count))
-    if not t.is_cuda:
-        raise ValueError("%s: not a GPU tensor" % name)
-    raise ValueError("%s: on device %d, the current one is %d" % (name, t.get_device(), device))
+def _native():
+    """The native marshalling of the small calls (csrc/tq_bind.cpp), on the library that is loaded here."""
+    global _native_module
+    if _native_module is None:
+        torch = _torch or _load_torch()
+        L = lib()
+        try:
+            from . import _tqbind
+        except ImportError as e:
+            raise RuntimeError("_tqbind.so is not built or does not load (%s); run `python -m ternary_weight_amd.build`"
+                               % e) from e
+        names = ("tq_rmsnorm", "tq_moe_dispatch", "tq_moe_combine", "tq_moe_combine_grad", "tq_gemm_dense_i8")
+        _tqbind.setup(*[ctypes.cast(getattr(L, n), _VP).value for n in names],
+                      getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream or _current_stream)
+        _native_module = _tqbind
+    return _native_module
 
 
 def desc(planes: int, group: int, scale_layout: int, out_features: int, in_features: int,
@@ -374,15 +371,13 @@ def ternarize_noalloc(d: tq_weight_desc, w, trits, scales, codebook=None, stream
                                       _stream(stream)), "tq_ternarize_noalloc")
 
 
+# The calls below check the tensors they are given (type, layout, length and
+# device: ValueError) besides what the C call checks.
 def rmsnorm(M, in_features, x_type, x, weight, eps, y_type, y, y_scale=None, residual_type=F32, residual=None,
             residual_out=None, stream=None):
     """RMSNorm with the residual's addition, to fp32, bf16 or int8 with a scale per token."""
-    n, r, dev = M * in_features, residual_type, _device()
-    _check(lib().tq_rmsnorm(M, in_features, x_type, _dense(x, "x", x_type, n, dev), residual_type,
-                            _dense(residual, "residual", r, n, dev), _dense(residual_out, "residual_out", r, n, dev),
-                            _dense(weight, "weight", F32, in_features, dev), eps, y_type,
-                            _dense(y, "y", y_type, n, dev), _dense(y_scale, "y_scale", F32, M if y_type == I8 else 0, dev),
-                            _stream(stream)), "tq_rmsnorm")
+    _check((_native_module or _native()).rmsnorm(M, in_features, x_type, x, residual_type, residual, residual_out, weight,
+                                                 eps, y_type, y, y_scale, stream), "tq_rmsnorm")
 
 
 def moe_dispatch_workspace_size(tokens, top_k, n_experts) -> int:
@@ -395,40 +390,25 @@ def moe_dispatch_workspace_size(tokens, top_k, n_experts) -> int:
 def moe_dispatch(tokens, top_k, n_experts, experts, rows, pairs, offsets, width=0, x_type=F32, x=None, x_scale=None,
                  xs=None, xs_scale=None, workspace=None, workspace_bytes=0, stream=None):
     """Sort the pairs (token, choice) by expert: the index arrays and, with x, the sorted rows."""
-    n, dev = tokens * top_k, _device()
-    ns = n if x_type == I8 and x is not None else 0
-    _check(lib().tq_moe_dispatch(tokens, top_k, n_experts, _dense(experts, "experts", "i32", n, dev), _dense(rows, "rows", "i32", n, dev),
-                                 _dense(pairs, "pairs", "i32", n, dev), _dense(offsets, "offsets", "i32", n_experts + 1, dev), width,
-                                 x_type, _dense(x, "x", x_type, tokens * width, dev),
-                                 _dense(x_scale, "x_scale", F32, tokens if ns else 0, dev), _dense(xs, "xs", x_type, n * width, dev),
-                                 _dense(xs_scale, "xs_scale", F32, ns, dev), _dense(workspace, "workspace", "any", workspace_bytes, dev),
-                                 workspace_bytes, _stream(stream)), "tq_moe_dispatch")
+    _check((_native_module or _native()).dispatch(tokens, top_k, n_experts, experts, rows, pairs, offsets, width, x_type, x,
+                                                  x_scale, xs, xs_scale, workspace_bytes, workspace, stream),
+           "tq_moe_dispatch")
 
 
 def moe_combine(tokens, top_k, width, n_rows, rows, weights, ys_type, ys, y_type, y, stream=None):
     """y[t] = sum_j weights[t][j] * ys[rows[t][j]]; weights None: ones."""
-    n, dev = tokens * top_k, _device()
-    _check(lib().tq_moe_combine(tokens, top_k, width, n_rows, _dense(rows, "rows", "i32", n, dev), _dense(weights, "weights", F32, n, dev),
-                                ys_type, _dense(ys, "ys", ys_type, n_rows * width, dev), y_type,
-                                _dense(y, "y", y_type, tokens * width, dev), _stream(stream)), "tq_moe_combine")
+    _check((_native_module or _native()).combine(tokens, top_k, width, n_rows, rows, weights, ys_type, ys, y_type, y, stream),
+           "tq_moe_combine")
 
 
 def moe_combine_grad(tokens, top_k, width, n_rows, rows, weights, dy_type, dy, ys_type, ys, d_ys=None, d_weights=None,
                      stream=None):
     """The gradient of moe_combine in ys and weights (either may be None)."""
-    n, m, dev = tokens * top_k, n_rows * width, _device()
-    _check(lib().tq_moe_combine_grad(tokens, top_k, width, n_rows, _dense(rows, "rows", "i32", n, dev),
-                                     _dense(weights, "weights", F32, n, dev), dy_type,
-                                     _dense(dy, "dy", dy_type, tokens * width, dev), ys_type,
-                                     _dense(ys, "ys", ys_type, m if d_weights is not None else 0, dev),
-                                     _dense(d_ys, "d_ys", ys_type, m, dev), _dense(d_weights, "d_weights", F32, n, dev),
-                                     _stream(stream)), "tq_moe_combine_grad")
+    _check((_native_module or _native()).combine_grad(tokens, top_k, width, n_rows, rows, weights, dy_type, dy, ys_type, ys,
+                                                      d_ys, d_weights, stream), "tq_moe_combine_grad")
 
 
 def gemm_dense_i8(M, N, in_features, xq, x_scale, w, w_scale, y_type, y, stream=None):
     """Product of int8 activations with a dense int8 weight, a scale per token and per output channel."""
-    dev = _device()
-    _check(lib().tq_gemm_dense_i8(M, N, in_features, _dense(xq, "xq", I8, M * in_features, dev),
-                                  _dense(x_scale, "x_scale", F32, M, dev), _dense(w, "w", I8, N * in_features, dev),
-                                  _dense(w_scale, "w_scale", F32, N, dev), y_type, _dense(y, "y", y_type, M * N, dev),
-                                  _stream(stream)), "tq_gemm_dense_i8")
+    _check((_native_module or _native()).gemm_dense_i8(M, N, in_features, xq, x_scale, w, w_scale, y_type, y, stream),
+           "tq_gemm_dense_i8")

@@ -134,4 +134,15 @@ def test_binding_checks_tensors():
         tq.moe_combine_grad(4, 2, 64, 8, A, B, tq.F32, C, tq.F32, D, E, torch.zeros(7), stream=0)
     with pytest.raises(tq.TQError):
         tq.gemm_dense_i8(1, 1, 8, A, B, C, D, tq.F32, E, stream=0)
+    for bad, error in (([1.0], TypeError), ("x", TypeError)):
+        with pytest.raises(error):
+            tq.rmsnorm(1, 16, tq.F32, bad, B, 1e-5, tq.F32, C, stream=0)
+    with pytest.raises(OverflowError):
+        tq.rmsnorm(1, 16, 1 << 40, A, B, 1e-5, tq.F32, C, stream=0)
+    with pytest.raises(ValueError, match="xq: 16 elements, needs"):          # a count past 64 bits
+        tq.gemm_dense_i8(1 << 60, 1, 1 << 20, torch.zeros(16, dtype=torch.int8), A, B, C, tq.F32, D, stream=0)
+    for call in (lambda: tq.rmsnorm(None, 16, tq.F32, A, B, 1e-5, tq.F32, C, stream=0),
+                 lambda: tq.moe_combine(1, 1, 16, 1, A, B, tq.F32, C, tq.F32, D, stream=object())):
+        with pytest.raises((TypeError, AttributeError)):
+            call()
     assert ctypes.sizeof(ctypes.c_void_p) == 8
