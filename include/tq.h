@@ -567,8 +567,9 @@ tq_status tq_moe_combine(int64_t tokens, int32_t top_k, int64_t width, int64_t n
  * Either output may be NULL (not computed; ys is needed only for d_weights,
  * weights only for d_ys, where NULL stands for weights of one).  tq_moe_dispatch
  * gives every pair a row of its own; with other index arrays, a row that
- * several pairs name is unspecified in d_ys.  Limits and alignment as in tq_moe_combine, d_ys 16-byte
- * aligned; outputs must not overlap another array (TQ_ERR_ARG).
+ * several pairs name is unspecified in d_ys.  Limits and alignment as in
+ * tq_moe_combine, d_ys 16-byte aligned; outputs must not overlap another array
+ * (TQ_ERR_ARG).
  */
 tq_status tq_moe_combine_grad(int64_t tokens, int32_t top_k, int64_t width, int64_t n_rows, const int32_t* rows,
                               const float* weights, int32_t dy_type, const void* dy, int32_t ys_type, const void* ys,

@@ -41,7 +41,10 @@ bool type_fits(at::ScalarType t, int64_t kind)
 
 const char* type_name(int64_t kind)
 {
-    return kind == TQ_F32 ? "torch.float32" : kind == TQ_BF16 ? "torch.bfloat16" : kind == TQ_I8 ? "torch.int8" : "torch.int32";
+    return kind == TQ_F32    ? "torch.float32"
+           : kind == TQ_BF16 ? "torch.bfloat16"
+           : kind == TQ_I8   ? "torch.int8"
+                             : "torch.int32";
 }
 
 // a * b elements; past 64 bits more than any tensor has.
@@ -130,11 +133,13 @@ struct Call {
                 if (s) PyErr_Format(PyExc_ValueError, "%s: not contiguous (strides %S)", name, s);
                 Py_XDECREF(s);
             } else if (t.numel() < count) {
-                PyErr_Format(PyExc_ValueError, "%s: %lld elements, needs %lld", name, (long long)t.numel(), (long long)count);
+                PyErr_Format(PyExc_ValueError, "%s: %lld elements, needs %lld", name, (long long)t.numel(),
+                             (long long)count);
             } else if (!is_gpu) {
                 PyErr_Format(PyExc_ValueError, "%s: not a GPU tensor", name);
             } else {
-                PyErr_Format(PyExc_ValueError, "%s: on device %d, the current one is %ld", name, (int)t.get_device(), device);
+                PyErr_Format(PyExc_ValueError, "%s: on device %d, the current one is %ld", name, (int)t.get_device(),
+                             device);
             }
         }
         bad = true;
@@ -228,6 +233,10 @@ PyObject* dispatch(PyObject*, PyObject* const* args, Py_ssize_t n)
         void* xs = c.array("xs", xt, count_of(P, H));
         float* xss = c.array<float>("xs_scale", TQ_F32, scales ? P : 0);
         const int64_t nws = c.integer();                   // before the workspace, whose length it is
+        if (nws < 0 && !c.bad) {
+            PyErr_Format(PyExc_ValueError, "workspace_bytes = %lld", (long long)nws);
+            c.bad = true;
+        }
         void* ws = c.array("workspace", KIND_ANY, nws);
         void* st = c.stream();
         return unlocked(c, [=] {

@@ -116,18 +116,20 @@ __global__ __launch_bounds__(64 * W) void k_dense_i8_few(Args A, int tiles_m, in
 // that the 8 lanes of one LDS pass (rows R .. R + 7 of one chunk) fall in
 // distinct banks.  Loads go from memory straight to LDS: a wave's load fills
 // 1 KiB in lane order (8 rows), so the swizzle is applied to the address that
-// each lane reads.  While the matrix cores run on one step's fragments those of
-// the next are read from LDS.  At the second step
-// of a stage the waves meet: the next stage has then arrived, and every
-// fragment of this one is in registers, so its place takes the loads of the
-// stage after the next, spread over the step's MFMAs.
-// The ring holds NS stages, NS - 1 of them requested ahead.  The columns are
+// each lane reads.  While the matrix cores run on one step's fragments those
+// of the next are read from LDS.  At the second step of a stage the waves
+// meet: the next stage has then arrived, and every fragment of this one is in
+// registers, so its place takes the loads of a stage further on, spread over
+// the step's MFMAs.
+//
+// The ring holds NS stages, all of them requested ahead.  The columns are
 // walked from the end: the first stage may be short, its x fragments past Kin
 // are set to zero, and it starts at the place of the ring from which whole
 // turns are left, so that the loop needs no masks and no tests.  KS groups of
 // 4 waves share a tile's columns, a block of 128 each in turn, and add their
 // sums in LDS.  Rows past M and N are read as the last row (their outputs are
 // not stored).
+//
 // 8192 x 14336 x 4096, bf16 out: 0.40 ms, 2.4 POP/s, the matrix cores busy 54%
 // of the time at the clock the power limit leaves (int8 MFMAs alone on random
 // values reach 3.2 to 3.9 POP/s, a library product of 8192^3 2.1 POP/s, this
@@ -170,8 +172,8 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
     constexpr int STAGE = (TM + TN) * 128;
     static_assert(NS >= 2 && NS <= 4, "stages in the ring");
     // an array per stage: the compiler then sees that a read of one does not wait for the loads into another
-    __shared__ __attribute__((aligned(1024))) uint8_t st0_[KS * STAGE], st1_[KS * STAGE], st2_[NS > 2 ? KS * STAGE : 16],
-        st3_[NS > 3 ? KS * STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t st0_[KS * STAGE], st1_[KS * STAGE],
+        st2_[NS > 2 ? KS * STAGE : 16], st3_[NS > 3 ? KS * STAGE : 16];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave_id & 3, group = wave_id >> 2;
     uint8_t* const st0 = st0_ + group * STAGE;
@@ -222,8 +224,8 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
     // A row of MFMAs covers the reads of one x and one w fragment and, spread, a load or two: all of a step's loads at
     // once hold the wave at their issue while its matrix core idles (4096 x 4096 x 4096: 3 per row 59.8, 4 per row
     // 65.8 us, against 55.9).
-    auto step = [&](bool second, const i32x4 (&x)[FM], const i32x4 (&w)[FN], const uint8_t* next, int at, i32x4 (&xn)[FM],
-                    i32x4 (&wn)[FN], uint8_t* free, int j) __attribute__((always_inline)) {
+    auto step = [&](bool second, const i32x4 (&x)[FM], const i32x4 (&w)[FN], const uint8_t* next, int at,
+                    i32x4 (&xn)[FM], i32x4 (&wn)[FN], uint8_t* free, int j) __attribute__((always_inline)) {
         if (second) {
             wait_vm<(NS - 2) * NL>();                     // the next stage's loads have arrived ..
             __builtin_amdgcn_s_waitcnt(0xC07F);           // .. and lgkmcnt(0): this one's reads are done
@@ -276,7 +278,8 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
             if ((place < skip) != wrapped) return;
             // columns past Kin in the last block are read from its first chunk, a block past Kin is the one before it
             const bool first = !wrapped && place == skip, none = first && valid == 0;
-            request(st, none ? 1 : place - skip + (wrapped ? NS : 0), first && !none && 16 * c >= valid ? 16 * c : 0, 0, NL);
+            request(st, none ? 1 : place - skip + (wrapped ? NS : 0), first && !none && 16 * c >= valid ? 16 * c : 0, 0,
+                    NL);
         };
         begin(0, st0, false);
         begin(1, st1, false);
@@ -380,9 +383,9 @@ struct Kernel {
     double turn, setup, busy, wg, stream, base;
 };
 #define TQ_DENSE_FEW(W) {k_dense_i8_few<TQ_F32, W>, k_dense_i8_few<TQ_BF16, W>, 16, 16, W, 64 * W, 4
-#define TQ_DENSE_TILE(FM, FN, KS, NS, RES)                                                                           \
-    {k_dense_i8_tile<TQ_F32, FM, FN, KS, NS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS, NS>, 32 * FM, 32 * FN, KS, 256 * KS, \
-     RES
+#define TQ_DENSE_TILE(FM, FN, KS, NS, RES)                                                                        \
+    {k_dense_i8_tile<TQ_F32, FM, FN, KS, NS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS, NS>, 32 * FM, 32 * FN, KS, \
+     256 * KS, RES
 const Kernel kKernels[] = {
     TQ_DENSE_FEW(4),              0.027, 1.153, 0.297, 0.000, 1.038, 2.994},     // M <= 16 only
     TQ_DENSE_TILE(1, 1, 1, 4, 5), 0.000, 1.401, 0.114, 0.336, 0.968, 2.847},
@@ -434,7 +437,8 @@ TQ_EXPORT tq_status tq_gemm_dense_i8(int64_t M, int64_t N, int64_t Kin, const in
     if (y_type != TQ_F32 && y_type != TQ_BF16)
         return tq_fail(TQ_ERR_ARG, "y_type = %d, must be TQ_F32 or TQ_BF16", y_type);
     if (Kin % 16 || Kin > TQ_MAX_KIN || M > TQ_MAX_N || N > TQ_MAX_N)
-        return tq_fail(TQ_ERR_SHAPE, "M = %lld, N = %lld, in_features = %lld: M and N up to %d, Kin a multiple of 16 up to %d",
+        return tq_fail(TQ_ERR_SHAPE,
+                       "M = %lld, N = %lld, in_features = %lld: M and N up to %d, Kin a multiple of 16 up to %d",
                        (long long)M, (long long)N, (long long)Kin, TQ_MAX_N, TQ_MAX_KIN);
     if (M == 0 || N == 0) return tq_ok();
     if ((s = tq_check_ptr(xq, "xq", Kin == 0))) return s;

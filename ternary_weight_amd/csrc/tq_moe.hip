@@ -23,8 +23,8 @@ constexpr int kSmallExperts = 960;            // ... if its counters (16 waves b
 constexpr int64_t kBlockPairs = 2048;         // the two-launch sort's pairs per workgroup, at least: with 1024 threads
 constexpr int kMaxBlocks = 256;               // 65536 pairs take 10 us (256 threads and 1024 pairs: 13 us)
 constexpr int kMaxGrid = 1 << 20;             // workgroups of one launch; more tokens are walked in a loop
-constexpr int64_t kFewPairs = 1024;           // up to here every wave finds its own rows (64 tokens, top 8: 5.7 us, 9.3 us
-                                              // with a sort before the copy; 2048 pairs 11.0 against 8.8 us)
+constexpr int64_t kFewPairs = 1024;           // up to here every wave finds its own rows (64 tokens, top 8: 5.7 us,
+                                              // 9.3 us with a sort first; 2048 pairs 11.0 against 8.8 us)
 
 // Lanes of the wave (active ones) whose bucket equals this lane's: one
 // ballot per bit of the bucket.
@@ -114,17 +114,17 @@ __device__ __forceinline__ void place_runs(const int32_t* experts, int64_t p0, i
             rows[p] = e < E ? row : -1;
             pairs[row] = e < E ? (int32_t)p : -1;
         }
-        // the bucket's first lane moves the counter on, after every lane has read it
-        __builtin_amdgcn_wave_barrier();
+        // the bucket's first lane moves the counter on, after every lane has read it and before any reads it again
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (on && (same & below) == 0) mine[e] += __popcll(same);
-        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
 // One workgroup sorts every pair.
-__global__ __launch_bounds__(kSortThreads) void k_sort_one(const int32_t* __restrict__ experts, int64_t P, int E, int bits,
-                                                           int32_t* __restrict__ rows, int32_t* __restrict__ pairs,
-                                                           int32_t* __restrict__ offsets)
+__global__ __launch_bounds__(kSortThreads) void k_sort_one(const int32_t* __restrict__ experts, int64_t P, int E,
+                                                           int bits, int32_t* __restrict__ rows,
+                                                           int32_t* __restrict__ pairs, int32_t* __restrict__ offsets)
 {
     extern __shared__ int cnt[];
     constexpr int W = kSortThreads / 64;
@@ -238,9 +238,9 @@ __global__ __launch_bounds__(T) void k_sort_place(const int32_t* __restrict__ ex
 // In the row kernels a wave has one token and a run of 64 (k_combine: 64 V)
 // units of 16 bytes of its row; a workgroup's 4 waves have 4 / W tokens and W
 // neighbouring runs (W = 1 << lw; a row's runs at the same time, or memory
-// pages are opened for each), blockIdx.y the next W.  The token is the same in all lanes,
-// and told so to the compiler: row numbers and weights come through scalar
-// loads.
+// pages are opened for each), blockIdx.y the next W.  The token is the same
+// in all lanes, and told so to the compiler: row numbers and weights come
+// through scalar loads.
 __device__ __forceinline__ int64_t first_token(int lw)
 {
     return ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) >> lw;
@@ -631,8 +631,8 @@ void sort_in_two(const int32_t* experts, int64_t P, int E, int bits, int32_t* co
     const unsigned n = (unsigned)sort_blocks(P, &per);
     const size_t lds = T / 64 * (E + 1) * 4;
     hipLaunchKernelGGL(k_sort_count<T>, dim3(n), dim3(T), lds, st, experts, P, per, E, counts);
-    hipLaunchKernelGGL(k_sort_place<T>, dim3(n), dim3(T), lds, st, experts, P, per, E, bits, (const int32_t*)counts, rows,
-                       pairs, offsets);
+    hipLaunchKernelGGL(k_sort_place<T>, dim3(n), dim3(T), lds, st, experts, P, per, E, bits, (const int32_t*)counts,
+                       rows, pairs, offsets);
 }
 
 }  // namespace
@@ -703,8 +703,8 @@ TQ_EXPORT tq_status tq_moe_dispatch(int64_t tokens, int32_t top_k, int32_t n_exp
         return tq_ok();
     }
     if (need == 0) {
-        hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kSortThreads), kSortThreads / 64 * (n_experts + 1) * 4, st, experts,
-                           P, n_experts, bits, rows, pairs, offsets);
+        hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kSortThreads), kSortThreads / 64 * (n_experts + 1) * 4, st,
+                           experts, P, n_experts, bits, rows, pairs, offsets);
     } else {
         // 16 waves' counters of n_experts + 1 buckets within 64 KiB of LDS, or 8 waves'
         const auto sort = n_experts <= kSmallExperts ? sort_in_two<1024> : sort_in_two<512>;
@@ -727,8 +727,8 @@ void launch_combine_as(int64_t tokens, int top_k, int64_t units, int64_t n_rows,
 {
     int lw;
     const dim3 grid = row_grid(tokens, units, V, &lw);
-    hipLaunchKernelGGL((k_combine<ST, YT, J, V>), grid, dim3(256), 0, st, tokens, top_k, units, lw, n_rows, rows, weights, ys,
-                       y);
+    hipLaunchKernelGGL((k_combine<ST, YT, J, V>), grid, dim3(256), 0, st, tokens, top_k, units, lw, n_rows, rows, weights,
+                       ys, y);
 }
 
 // 16 loads of 16 bytes in flight per lane: over the pairs, then along the row.
@@ -749,11 +749,11 @@ void launch_grad(int64_t tokens, int top_k, int64_t width, int64_t n_rows, const
 {
     const int64_t units = width / unit_of<ST>();
     if (units <= 64)
-        hipLaunchKernelGGL((k_combine_grad<DT, ST, 1>), dim3(grid_of(tokens, 4)), dim3(256), 0, st, tokens, top_k, units,
-                           n_rows, rows, weights, dy, ys, d_ys, d_weights);
+        hipLaunchKernelGGL((k_combine_grad<DT, ST, 1>), dim3(grid_of(tokens, 4)), dim3(256), 0, st, tokens, top_k,
+                           units, n_rows, rows, weights, dy, ys, d_ys, d_weights);
     else    // 4099 tokens, 8 rows of 2048 bf16: 57.9 us; with one wave per token and two units per lane 71 us
-        hipLaunchKernelGGL((k_combine_grad<DT, ST, 4>), dim3(grid_of(tokens, 1)), dim3(256), 0, st, tokens, top_k, units,
-                           n_rows, rows, weights, dy, ys, d_ys, d_weights);
+        hipLaunchKernelGGL((k_combine_grad<DT, ST, 4>), dim3(grid_of(tokens, 1)), dim3(256), 0, st, tokens, top_k,
+                           units, n_rows, rows, weights, dy, ys, d_ys, d_weights);
 }
 
 }  // namespace
@@ -773,7 +773,8 @@ TQ_EXPORT tq_status tq_moe_combine(int64_t tokens, int32_t top_k, int64_t width,
     if ((s = tq_check_ptr(y, "y", false))) return s;
     const int64_t P = tokens * top_k;
     const Span out[] = {{y, tokens * width * size_of(y_type), "y"}};
-    const Span in[] = {{rows, P * 4, "rows"}, {weights, P * 4, "weights"}, {ys, n_rows * width * size_of(ys_type), "ys"}};
+    const Span in[] = {{rows, P * 4, "rows"}, {weights, P * 4, "weights"},
+                       {ys, n_rows * width * size_of(ys_type), "ys"}};
     if ((s = check_spans(out, in))) return s;
     auto* fn = ys_type == TQ_F32 ? (y_type == TQ_F32 ? launch_combine<TQ_F32, TQ_F32> : launch_combine<TQ_F32, TQ_BF16>)
                                  : (y_type == TQ_F32 ? launch_combine<TQ_BF16, TQ_F32> : launch_combine<TQ_BF16, TQ_BF16>);
@@ -799,7 +800,8 @@ TQ_EXPORT tq_status tq_moe_combine_grad(int64_t tokens, int32_t top_k, int64_t w
     if ((s = tq_check_ptr(d_weights, "d_weights", true, 4))) return s;
     const int64_t P = tokens * top_k, row = width * size_of(ys_type);
     const Span out[] = {{d_ys, n_rows * row, "d_ys"}, {d_weights, P * 4, "d_weights"}};
-    const Span in[] = {{rows, P * 4, "rows"}, {weights, P * 4, "weights"}, {dy, tokens * width * size_of(dy_type), "dy"},
+    const Span in[] = {{rows, P * 4, "rows"}, {weights, P * 4, "weights"},
+                       {dy, tokens * width * size_of(dy_type), "dy"},
                        {ys, d_weights ? n_rows * row : 0, "ys"}};
     if ((s = check_spans(out, in))) return s;
     auto* fn = dy_type == TQ_F32 ? (ys_type == TQ_F32 ? launch_grad<TQ_F32, TQ_F32> : launch_grad<TQ_F32, TQ_BF16>)

@@ -8,7 +8,7 @@
 // stand between reading x and writing y, so the row stays in registers
 // between them: a thread keeps V units of U consecutive elements, and the
 // row is read once, so memory bounds it (16381 x 4096, bf16 throughout with
-// the residual: 89.8 us, 5.98 TB/s, where a copy of 1 GiB reaches 5.15).
+// the residual: 89.6 us, 5.99 TB/s, where a copy of 1 GiB reaches 5.15).
 // The sum of squares is fp64 (an fp64 fma per element is far below the memory
 // time), rounded once to fp32; every other step is one IEEE fp32 operation
 // (this file is built with -ffp-contract=off), so the int8 codes equal
@@ -115,7 +115,10 @@ __device__ __forceinline__ float wave_max(float v)
 }
 
 // One row per workgroup of T threads, V units of U elements per thread; the
-// weight stays in registers over the workgroup's rows.
+// weight stays in registers over the workgroup's rows, except where a row
+// alone takes half of a thread's 128 registers (Kin > 32768): there it is read
+// from L2 again for each row, since keeping it spills (2048 x 65536, bf16
+// throughout with the residual: 213 us, 422 us with the weight kept).
 // Two reductions use two LDS arrays: a wave writes the first again only
 // after the second's barrier, which every wave reaches after reading the
 // first, so the loop over rows needs no further barrier.
@@ -123,13 +126,15 @@ template <int XT, int RT, int YT, int U, int T, int V>
 __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
 {
     constexpr int W = T / 64;
+    constexpr bool kKeep = V * U <= 32;
     __shared__ double red_s[W];
     __shared__ float red_a[W];
     const int tid = threadIdx.x, nu = A.Kin / U;
-    float w[V][U];
+    float w[kKeep ? V : 1][U];
+    if constexpr (kKeep)
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (tid + j * T < nu) load_u<TQ_F32, U>(A.w, tid + j * T, w[j]);
+        for (int j = 0; j < V; ++j)
+            if (tid + j * T < nu) load_u<TQ_F32, U>(A.w, tid + j * T, w[j]);
     for (int64_t m = blockIdx.x; m < A.M; m += gridDim.x) {
         const int64_t at = m * A.Kin;
         const uint8_t* xr = (const uint8_t*)A.x + at * (XT == TQ_F32 ? 4 : 2);
@@ -176,8 +181,9 @@ __global__ __launch_bounds__(T) void k_rmsnorm(Args A)
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (tid + j * T < nu) {
+                if constexpr (!kKeep) load_u<TQ_F32, U>(A.w, tid + j * T, w[0]);
 #pragma unroll
-                for (int e = 0; e < U; ++e) h[j][e] = (h[j][e] * r) * w[j][e];
+                for (int e = 0; e < U; ++e) h[j][e] = (h[j][e] * r) * w[kKeep ? j : 0][e];
                 if constexpr (YT != TQ_I8) {
                     store_u<YT, U>((uint8_t*)A.y + at * (YT == TQ_F32 ? 4 : 2), tid + j * T, h[j]);
                 } else {
@@ -234,12 +240,14 @@ void launch(const Args& A, hipStream_t st)
         else if (A.Kin <= 4096) launch_as<XT, RT, YT, 8, 256, 2>(A, st);
         else if (A.Kin <= 8192) launch_as<XT, RT, YT, 8, 256, 4>(A, st);
         else if (A.Kin <= 16384) launch_as<XT, RT, YT, 8, 512, 4>(A, st);
+        else if (A.Kin <= 32768) launch_as<XT, RT, YT, 8, 1024, 4>(A, st);
         else launch_as<XT, RT, YT, 8, 1024, 8>(A, st);
     } else {
         if (A.Kin <= 1024) launch_as<XT, RT, YT, 4, 64, 4>(A, st);
         else if (A.Kin <= 4096) launch_as<XT, RT, YT, 4, 256, 4>(A, st);
         else if (A.Kin <= 8192) launch_as<XT, RT, YT, 4, 256, 8>(A, st);
         else if (A.Kin <= 16384) launch_as<XT, RT, YT, 4, 512, 8>(A, st);
+        else if (A.Kin <= 32768) launch_as<XT, RT, YT, 4, 1024, 8>(A, st);
         else launch_as<XT, RT, YT, 4, 1024, 16>(A, st);
     }
 }
@@ -269,7 +277,8 @@ TQ_EXPORT tq_status tq_rmsnorm(int64_t M, int64_t Kin, int32_t x_type, const voi
                                int32_t y_type, void* y, float* y_scale, void* stream)
 {
     tq_status s;
-    if (M < 0 || Kin < 0) return tq_fail(TQ_ERR_ARG, "negative size M = %lld, Kin = %lld", (long long)M, (long long)Kin);
+    if (M < 0 || Kin < 0)
+        return tq_fail(TQ_ERR_ARG, "negative size M = %lld, Kin = %lld", (long long)M, (long long)Kin);
     if (x_type != TQ_F32 && x_type != TQ_BF16)
         return tq_fail(TQ_ERR_ARG, "x_type = %d, must be TQ_F32 or TQ_BF16", x_type);
     if (residual && residual_type != TQ_F32 && residual_type != TQ_BF16)
@@ -279,7 +288,8 @@ TQ_EXPORT tq_status tq_rmsnorm(int64_t M, int64_t Kin, int32_t x_type, const voi
     if (Kin % 16 || Kin == 0 || Kin > TQ_MAX_KIN || M > (1ll << 31) - 1)
         return tq_fail(TQ_ERR_SHAPE, "M = %lld, in_features = %lld: a multiple of 16 in 16..%d, M up to 2^31 - 1",
                        (long long)M, (long long)Kin, TQ_MAX_KIN);
-    if (!(eps >= 0.0f) || isinf(eps)) return tq_fail(TQ_ERR_VALUE, "eps = %g, must be finite and not negative", (double)eps);
+    if (!(eps >= 0.0f) || isinf(eps))
+        return tq_fail(TQ_ERR_VALUE, "eps = %g, must be finite and not negative", (double)eps);
     if (residual_out && !residual) return tq_fail(TQ_ERR_ARG, "residual_out without a residual");
     if (M == 0) return tq_ok();
     if ((s = tq_check_ptr(x, "x", false))) return s;

@@ -376,8 +376,8 @@ def ternarize_noalloc(d: tq_weight_desc, w, trits, scales, codebook=None, stream
 def rmsnorm(M, in_features, x_type, x, weight, eps, y_type, y, y_scale=None, residual_type=F32, residual=None,
             residual_out=None, stream=None):
     """RMSNorm with the residual's addition, to fp32, bf16 or int8 with a scale per token."""
-    _check((_native_module or _native()).rmsnorm(M, in_features, x_type, x, residual_type, residual, residual_out, weight,
-                                                 eps, y_type, y, y_scale, stream), "tq_rmsnorm")
+    _check((_native_module or _native()).rmsnorm(M, in_features, x_type, x, residual_type, residual, residual_out,
+                                                 weight, eps, y_type, y, y_scale, stream), "tq_rmsnorm")
 
 
 def moe_dispatch_workspace_size(tokens, top_k, n_experts) -> int:
@@ -390,22 +390,22 @@ def moe_dispatch_workspace_size(tokens, top_k, n_experts) -> int:
 def moe_dispatch(tokens, top_k, n_experts, experts, rows, pairs, offsets, width=0, x_type=F32, x=None, x_scale=None,
                  xs=None, xs_scale=None, workspace=None, workspace_bytes=0, stream=None):
     """Sort the pairs (token, choice) by expert: the index arrays and, with x, the sorted rows."""
-    _check((_native_module or _native()).dispatch(tokens, top_k, n_experts, experts, rows, pairs, offsets, width, x_type, x,
-                                                  x_scale, xs, xs_scale, workspace_bytes, workspace, stream),
+    _check((_native_module or _native()).dispatch(tokens, top_k, n_experts, experts, rows, pairs, offsets, width, x_type,
+                                                  x, x_scale, xs, xs_scale, workspace_bytes, workspace, stream),
            "tq_moe_dispatch")
 
 
 def moe_combine(tokens, top_k, width, n_rows, rows, weights, ys_type, ys, y_type, y, stream=None):
     """y[t] = sum_j weights[t][j] * ys[rows[t][j]]; weights None: ones."""
-    _check((_native_module or _native()).combine(tokens, top_k, width, n_rows, rows, weights, ys_type, ys, y_type, y, stream),
-           "tq_moe_combine")
+    _check((_native_module or _native()).combine(tokens, top_k, width, n_rows, rows, weights, ys_type, ys, y_type, y,
+                                                 stream), "tq_moe_combine")
 
 
 def moe_combine_grad(tokens, top_k, width, n_rows, rows, weights, dy_type, dy, ys_type, ys, d_ys=None, d_weights=None,
                      stream=None):
     """The gradient of moe_combine in ys and weights (either may be None)."""
-    _check((_native_module or _native()).combine_grad(tokens, top_k, width, n_rows, rows, weights, dy_type, dy, ys_type, ys,
-                                                      d_ys, d_weights, stream), "tq_moe_combine_grad")
+    _check((_native_module or _native()).combine_grad(tokens, top_k, width, n_rows, rows, weights, dy_type, dy,
+                                                      ys_type, ys, d_ys, d_weights, stream), "tq_moe_combine_grad")
 
 
 def gemm_dense_i8(M, N, in_features, xq, x_scale, w, w_scale, y_type, y, stream=None):

@@ -10,7 +10,7 @@ from tests import operator_ref as ref
 pytestmark = pytest.mark.gpu
 EPS = 1e-5
 # widths around the edges of every kernel shape: one wave, workgroups, the widest row
-WIDTHS = [16, 48, 64, 256, 272, 1008, 1024, 1040, 2048, 2560, 4096, 4112, 6912, 8192, 8208, 14336, 16384, 16400, 65536]
+WIDTHS = [16, 48, 64, 256, 272, 1008, 1024, 1040, 2048, 2560, 4096, 4112, 6912, 8192, 8208, 14336, 16384, 16400, 32768, 32784, 65536]
 
 
 def _torch():

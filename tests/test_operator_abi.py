@@ -146,3 +146,5 @@ def test_binding_checks_tensors():
         with pytest.raises((TypeError, AttributeError)):
             call()
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+    with pytest.raises(ValueError, match="workspace_bytes = -1"):       # not the largest size_t
+        tq.moe_dispatch(10000, 2, 8, A, B, C, D, workspace=E, workspace_bytes=-1, stream=0)
