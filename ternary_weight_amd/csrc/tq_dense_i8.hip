@@ -54,7 +54,7 @@ __device__ __forceinline__ void store_quad(void* y, int64_t at, const float (&v)
 // waves of a compute unit together hold enough); non-temporal loads were 10%
 // slower.  Loads go through buffer resources: lanes past M, N or Kin read
 // zeros without touching memory.
-// 13 x 4096 x 14336: 17.9 us, 3.3 TB/s.
+// 13 x 4096 x 14336: 13.7 us, 4.3 TB/s.
 template <int YT, int W>
 __global__ __launch_bounds__(64 * W) void k_dense_i8_few(Args A, int tiles_m, int)
 {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * W) void k_dense_i8_few(Args A, int tiles_m, in
 // sums in LDS.  Rows past M and N are read as the last row (their outputs are
 // not stored).
 //
-// 8192 x 14336 x 4096, bf16 out: 0.40 ms, 2.4 POP/s, the matrix cores busy 54%
+// 8192 x 14336 x 4096, bf16 out: 0.41 ms, 2.3 POP/s, the matrix cores busy 54%
 // of the time at the clock the power limit leaves (int8 MFMAs alone on random
 // values reach 3.2 to 3.9 POP/s, a library product of 8192^3 2.1 POP/s, this
 // one 2.6); LDS reads without bank conflicts; what is left over is the
