@@ -112,6 +112,38 @@ def test_more_tokens_than_waves():
     assert torch.all((d_w.double() - dots).abs() <= 32 * ref.U24 * mag)
 
 
+def test_beyond_32_bit_offsets():
+    """2^31 elements and more in the sorted rows: there, back and the gradient."""
+    from ternary_weight_amd import tq
+    torch = _torch()
+    T, k, E, H = 16400, 2, 5, 65536
+    g = torch.Generator(device="cuda").manual_seed(12)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randint(-127, 128, (T, H), generator=g, device="cuda", dtype=torch.int8)
+    xsc = torch.rand(T, device="cuda", generator=g)
+    rows, pairs, offs, xs, xss = dispatch(ids.cpu().numpy(), E, H, I8, x, xsc)
+    P = T * k
+    for p0 in range(0, P, 4096):
+        t = pairs[p0:p0 + 4096].long() // k
+        assert torch.equal(xs[p0:p0 + len(t)], x[t]) and torch.equal(xss[p0:p0 + len(t)], xsc[t])
+    del x, xs
+    # small whole numbers: every product and sum is exact, in bf16 too
+    ys = torch.randint(-4, 5, (P, H), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    w = torch.randint(1, 4, (T, k), generator=g, device="cuda").float()
+    y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    tq.moe_combine(T, k, H, P, rows, w, BF16, ys, BF16, y)
+    dy = torch.randint(-3, 4, (T, H), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    d_ys, d_w = torch.empty_like(ys), torch.empty(T, k, device="cuda")
+    tq.moe_combine_grad(T, k, H, P, rows, w, BF16, dy, BF16, ys, d_ys, d_w)
+    for t0 in range(0, T, 1024):
+        t = slice(t0, min(t0 + 1024, T))
+        r = rows[t].long()
+        picked = ys[r.view(-1)].view(-1, k, H).float()
+        assert torch.equal(y[t].float(), (picked * w[t, :, None]).sum(1))
+        assert torch.equal(d_ys[r.view(-1)].view(-1, k, H).float(), dy[t, None].float() * w[t, :, None])
+        assert torch.equal(d_w[t], (picked * dy[t, None].float()).sum(2))
+
+
 @pytest.mark.parametrize("xt", [F32, BF16, I8])
 @pytest.mark.parametrize("T,k,E,H", [(300, 5, 9, 16400), (1, 1, 1, 16), (5, 3, 4, 48), (64, 8, 128, 2048), (200, 2, 9, 4112),
                                      (1500, 8, 33, 272), (7, 4, 6, 65536)])

@@ -99,7 +99,7 @@ def test_widths(K):
 @pytest.mark.parametrize("rt", [None, F32, BF16])
 @pytest.mark.parametrize("yt", [F32, BF16, I8])
 def test_types(xt, rt, yt):
-    for M, K in ((5, 720), (4, 2560), (2, 20480)):
+    for M, K in ((5, 720), (4, 2560), (2, 20480), (2, 40976)):
         check(M, K, xt, rt, yt)
         if rt is not None:
             check(M, K, xt, rt, yt, in_place=True)
@@ -127,6 +127,24 @@ def test_many_rows():
     rq, rs = ref.quant_steps(ns)
     assert np.array_equal(y.cpu().numpy(), ns)
     assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+
+
+def test_beyond_32_bit_offsets():
+    """2^31 elements and more: the last rows equal the same rows by themselves."""
+    from ternary_weight_amd import tq
+    torch = _torch()
+    M, K, n = 32800, 65536, 7
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    h = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.rand(K, device="cuda", generator=g)
+    tail, htail = x[M - n:].clone(), h[M - n:].clone()
+    q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    tq.rmsnorm(M, K, BF16, x, w, EPS, I8, q, s, BF16, h, h)
+    q2, s2 = torch.empty(n, K, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    tq.rmsnorm(n, K, BF16, tail, w, EPS, I8, q2, s2, BF16, htail, htail)
+    assert torch.equal(q[M - n:], q2) and torch.equal(s[M - n:], s2) and torch.equal(h[M - n:], htail)
+    assert torch.equal(x[M - n:], tail) and bool(torch.all(s > 0))
 
 
 def test_same_codes_as_the_quantiser():
@@ -197,7 +215,8 @@ def test_graph_and_streams():
     x, h, w = torch.randn(M, K, device="cuda", generator=g), torch.randn(M, K, device="cuda", generator=g), \
         torch.rand(K, device="cuda", generator=g)
     ho, q, s = torch.empty_like(h), torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
-    call = lambda st, out: tq.rmsnorm(M, K, F32, x, w, EPS, I8, out[0], out[1], residual=h, residual_out=out[2], stream=st)
+    call = lambda st, out: tq.rmsnorm(M, K, F32, x, w, EPS, I8, out[0], out[1], residual=h, residual_out=out[2],
+                                      stream=st)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     call(side, (q, s, ho))
