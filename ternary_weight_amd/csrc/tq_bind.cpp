@@ -1,7 +1,7 @@
 // Native marshalling of the binding's small calls (tq.rmsnorm, tq.moe_*,
 // tq.gemm_dense_i8): checks of the tensors and the C call, with no step of the
 // computation.  Through ctypes such a call took 6 to 8 us on the host, more
-// than its kernel on small inputs; here it takes about 4, the launch itself.
+// than its kernel on small inputs; here it takes 3 to 4, the launch itself.
 //
 // Every function takes the arguments of the C call in its order, with tensors
 // (or addresses, or None) for arrays, and returns the status.  Of a tensor it

@@ -407,7 +407,8 @@ double estimate(const Kernel& k, int64_t M, int64_t N, int64_t Kin, int64_t y_by
     const double q = k.resident == 1 ? ceil(x) : x < 1.0 ? 1.0 : x;
     const double own = ceil(x / k.resident) * (k.setup + k.turn * turns), work = q * (k.wg + k.busy * turns);
     const double mem = k.stream * (double)(N * Kin + M * Kin + y_bytes) / 5.2e6;
-    return k.base + pow(pow(own, 8.0) + pow(work, 8.0) + pow(mem, 8.0), 0.125);
+    const auto eighth = [](double v) { return v *= v, v *= v, v * v; };
+    return k.base + sqrt(sqrt(sqrt(eighth(own) + eighth(work) + eighth(mem))));
 }
 
 // The kernel for a product, or null where no launch holds its tiles.
