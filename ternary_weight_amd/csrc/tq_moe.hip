@@ -23,8 +23,9 @@ constexpr int kSmallExperts = 960;            // ... if its counters (16 waves b
 constexpr int64_t kBlockPairs = 2048;         // the two-launch sort's pairs per workgroup, at least: with 1024 threads
 constexpr int kMaxBlocks = 256;               // 65536 pairs take 10 us (256 threads and 1024 pairs: 13 us)
 constexpr int kMaxGrid = 1 << 20;             // workgroups of one launch; more tokens are walked in a loop
-constexpr int64_t kFewPairs = 1024;           // up to here every wave finds its own rows (64 tokens, top 8: 5.7 us,
-                                              // 9.3 us with a sort first; 2048 pairs 11.0 against 8.8 us)
+constexpr int64_t kFewPairs = 1024;           // up to here every wave finds its own rows (128 tokens, top 8: 5.4 us,
+                                              // 9.3 us with a sort first; 256 tokens 8.3 against 8.9 us, but the
+                                              // longer key list costs the smaller batches 1 us)
 
 // Lanes of the wave (active ones) whose bucket equals this lane's: one
 // ballot per bit of the bucket.
@@ -274,9 +275,12 @@ __global__ __launch_bounds__(256) void k_spread_rows(int64_t tokens, int top_k, 
     }
 }
 
-// Sort and copy in one launch, for few pairs.  A pair's row is how many pairs
-// have a smaller key bucket * P + pair: every wave counts that for its own
-// token's pairs, 64 keys per ballot.  The last workgroup finds the offsets.
+// Sort and copy in one launch, for few pairs (64 B at most).  A pair's row is
+// how many pairs have a smaller key bucket * P + pair: every wave counts that
+// for its own token's pairs, 64 keys per ballot, with all keys loaded at once
+// (64 tokens, top 8: 4.4 us, 5.8 us with four loads at a time; with B = 16 in
+// place of 8 4.8 us).  The last workgroup finds the offsets.
+template <int B>
 __global__ __launch_bounds__(256) void k_dispatch_few(const int32_t* __restrict__ experts, int tokens, int top_k, int E,
                                                       int32_t* __restrict__ rows, int32_t* __restrict__ pairs,
                                                       int32_t* __restrict__ offsets, int64_t units, int lw,
@@ -313,6 +317,14 @@ __global__ __launch_bounds__(256) void k_dispatch_few(const int32_t* __restrict_
     u32x4 v = {0, 0, 0, 0};
     if (u < units) v = x[t * units + u];
     constexpr int J = 8;
+    int k[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) k[b] = experts[b * 64 + lane < P ? b * 64 + lane : P - 1];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const int p = b * 64 + lane;
+        k[b] = p < P ? (k[b] >= 0 && k[b] < E ? k[b] : E) * P + p : INT32_MAX;
+    }
     for (int j0 = 0; j0 < top_k; j0 += J) {
         int key[J], row[J];
 #pragma unroll
@@ -321,13 +333,11 @@ __global__ __launch_bounds__(256) void k_dispatch_few(const int32_t* __restrict_
             key[j] = bucket_of(experts, p, E) * P + p;
             row[j] = 0;
         }
-#pragma unroll 4
-        for (int b = 0; b < P; b += 64) {
-            const int p = b + lane;
-            const int k = p < P ? bucket_of(experts, p, E) * P + p : INT32_MAX;
 #pragma unroll
-            for (int j = 0; j < J; ++j) row[j] += __popcll(__ballot(k < key[j]));
-        }
+        for (int b = 0; b < B; ++b)
+            if (b * 64 < P)
+#pragma unroll
+                for (int j = 0; j < J; ++j) row[j] += __popcll(__ballot(k[b] < key[j]));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             if (j0 + j >= top_k) break;
@@ -697,8 +707,9 @@ TQ_EXPORT tq_status tq_moe_dispatch(int64_t tokens, int32_t top_k, int32_t n_exp
     dim3 grid = row_grid(tokens, units, 1, &lw);
     if (P <= kFewPairs) {
         ++grid.x;
-        hipLaunchKernelGGL(k_dispatch_few, grid, dim3(256), 0, st, experts, (int)tokens, top_k, n_experts, rows, pairs,
-                           offsets, units, lw, xp, xsc, (u32x4*)xs, xs_scale);
+        const auto few = P <= 256 ? k_dispatch_few<4> : P <= 512 ? k_dispatch_few<8> : k_dispatch_few<kFewPairs / 64>;
+        hipLaunchKernelGGL(few, grid, dim3(256), 0, st, experts, (int)tokens, top_k, n_experts, rows, pairs, offsets,
+                           units, lw, xp, xsc, (u32x4*)xs, xs_scale);
         if ((s = tq_check_launch("tq_moe_dispatch"))) return s;
         return tq_ok();
     }
