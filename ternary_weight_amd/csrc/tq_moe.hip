@@ -22,6 +22,7 @@ constexpr int64_t kSmallPairs = 8192;         // up to here one workgroup sorts 
 constexpr int kSmallExperts = 960;            // ... if its counters (16 waves by n_experts + 1) fit 64 KiB of LDS
 constexpr int64_t kBlockPairs = 2048;         // the two-launch sort's pairs per workgroup, at least: with 1024 threads
 constexpr int kMaxBlocks = 256;               // 65536 pairs take 10 us (256 threads and 1024 pairs: 13 us)
+constexpr int kChunk = 2;                     // loads of ids at once in the sorts (4 measured alike, 8 slower)
 constexpr int kMaxGrid = 1 << 20;             // workgroups of one launch; more tokens are walked in a loop
 constexpr int64_t kFewPairs = 1024;           // up to here every wave finds its own rows (128 tokens, top 8: 5.4 us,
                                               // 9.3 us with a sort first; 256 tokens 8.3 against 8.9 us, but the
@@ -39,10 +40,33 @@ __device__ __forceinline__ uint64_t match_bucket(int b, int bits, bool active)
     return m;
 }
 
-__device__ __forceinline__ int bucket_of(const int32_t* experts, int64_t p, int E)
+__device__ __forceinline__ int bucket(int e, int E) { return e >= 0 && e < E ? e : E; }
+__device__ __forceinline__ int bucket_of(const int32_t* experts, int64_t p, int E) { return bucket(experts[p], E); }
+
+// The lane's ids of the 64 kChunk pairs from q on, loaded at once (from b on
+// the last one's before b).
+__device__ __forceinline__ void load_chunk(const int32_t* experts, int64_t q, int64_t b, int (&e)[kChunk])
 {
-    const int e = experts[p];
-    return e >= 0 && e < E ? e : E;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+        const int64_t p = q + 64 * i + (threadIdx.x & 63);
+        e[i] = experts[p < b ? p : b - 1];
+    }
+}
+
+// A bucket's counts per wave become the first rows of each wave's pairs, from
+// `at` on (all read before any is written: one latency).
+template <int W>
+__device__ __forceinline__ void firsts_of(int* cnt, int E, int e, int at)
+{
+    int c[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) c[w] = cnt[w * (E + 1) + e];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        cnt[w * (E + 1) + e] = at;
+        at += c[w];
+    }
 }
 
 // Exclusive sum over the workgroup's threads; *total gets the whole sum.
@@ -89,7 +113,14 @@ __device__ __forceinline__ void count_runs(const int32_t* experts, int64_t p0, i
     int64_t a, b;
     run_of_wave<T>(p0, p1, &a, &b);
     int* mine = cnt + (threadIdx.x >> 6) * (E + 1);
-    for (int64_t p = a + (threadIdx.x & 63); p < b; p += 64) atomicAdd(&mine[bucket_of(experts, p, E)], 1);
+    const int lane = threadIdx.x & 63;
+    for (int64_t q = a; q < b; q += 64 * kChunk) {
+        int e[kChunk];
+        load_chunk(experts, q, b, e);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if (q + 64 * i + lane < b) atomicAdd(&mine[bucket(e[i], E)], 1);
+    }
     __syncthreads();
 }
 
@@ -104,21 +135,27 @@ __device__ __forceinline__ void place_runs(const int32_t* experts, int64_t p0, i
     int* mine = cnt + (threadIdx.x >> 6) * (E + 1);
     const int lane = threadIdx.x & 63;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (int64_t q = a; q < b; q += 64) {
-        const int64_t p = q + lane;
-        const bool on = p < b;
-        const int e = on ? bucket_of(experts, p, E) : E;
-        const uint64_t same = match_bucket(e, bits, on);
-        if (on) {
-            const int rank = __popcll(same & below);
-            const int row = mine[e] + rank;
-            rows[p] = e < E ? row : -1;
-            pairs[row] = e < E ? (int32_t)p : -1;
+    for (int64_t c = a; c < b; c += 64 * kChunk) {
+        int ids[kChunk];
+        load_chunk(experts, c, b, ids);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const int64_t q = c + 64 * i, p = q + lane;
+            if (q >= b) break;
+            const bool on = p < b;
+            const int e = bucket(ids[i], E);
+            const uint64_t same = match_bucket(e, bits, on);
+            if (on) {
+                const int rank = __popcll(same & below);
+                const int row = mine[e] + rank;
+                rows[p] = e < E ? row : -1;
+                pairs[row] = e < E ? (int32_t)p : -1;
+            }
+            // the bucket's first lane moves the counter on, after every lane has read it and before any reads it again
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (on && (same & below) == 0) mine[e] += __popcll(same);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-        // the bucket's first lane moves the counter on, after every lane has read it and before any reads it again
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (on && (same & below) == 0) mine[e] += __popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -133,26 +170,18 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_one(const int32_t* __rest
     const int e = threadIdx.x;                       // E <= kSortThreads buckets, one per thread
     int sum = 0;
     if (e < E)
+#pragma unroll
         for (int w = 0; w < W; ++w) sum += cnt[w * (E + 1) + e];
     int total = 0;
     const int first = block_scan<kSortThreads>(sum, &total);
     if (e < E) {
         offsets[e] = first;
-        int at = first;
-        for (int w = 0; w < W; ++w) {
-            const int c = cnt[w * (E + 1) + e];
-            cnt[w * (E + 1) + e] = at;
-            at += c;
-        }
+        firsts_of<W>(cnt, E, e, first);
     }
-    if (e == 0) {
+    static_assert(kSmallExperts < kSortThreads, "the last thread has no expert");
+    if (e == kSortThreads - 1) {
         offsets[E] = total;
-        int at = total;
-        for (int w = 0; w < W; ++w) {
-            const int c = cnt[w * (E + 1) + E];
-            cnt[w * (E + 1) + E] = at;
-            at += c;
-        }
+        firsts_of<W>(cnt, E, E, total);
     }
     __syncthreads();
     place_runs<kSortThreads>(experts, 0, P, E, bits, cnt, rows, pairs);
@@ -169,6 +198,7 @@ __global__ __launch_bounds__(T) void k_sort_count(const int32_t* __restrict__ ex
     count_runs<T>(experts, p0, p1, E, cnt);
     for (int e = threadIdx.x; e <= E; e += T) {
         int s = 0;
+#pragma unroll
         for (int w = 0; w < T / 64; ++w) s += cnt[w * (E + 1) + e];
         counts[(int64_t)e * gridDim.x + blockIdx.x] = s;
     }
@@ -212,12 +242,7 @@ __global__ __launch_bounds__(T) void k_sort_place(const int32_t* __restrict__ ex
         const int e = threadIdx.x * n + k;
         if (k < n && e < E) {
             if (me == 0) offsets[e] = first;
-            int at = first + before[k];
-            for (int w = 0; w < W; ++w) {
-                const int c = cnt[w * (E + 1) + e];
-                cnt[w * (E + 1) + e] = at;
-                at += c;
-            }
+            firsts_of<W>(cnt, E, e, first + before[k]);
         }
         first += all[k];
     }
@@ -225,12 +250,7 @@ __global__ __launch_bounds__(T) void k_sort_place(const int32_t* __restrict__ ex
         if (me == 0) offsets[E] = total;
         int none, at;
         sums(E, &none, &at);
-        at += total;
-        for (int w = 0; w < W; ++w) {
-            const int c = cnt[w * (E + 1) + E];
-            cnt[w * (E + 1) + E] = at;
-            at += c;
-        }
+        firsts_of<W>(cnt, E, E, total + at);
     }
     __syncthreads();
     place_runs<T>(experts, p0, p1, E, bits, cnt, rows, pairs);
@@ -255,7 +275,7 @@ __device__ __forceinline__ int run_of(int lw)
 
 // Copy each token's row to its places: read once, written top_k times, one
 // unit per lane (2 and 4 were slower).  8192 tokens (5% of them padding), top
-// 8, 2048 bf16: 51 us, 5.6 TB/s, and 62 us with the sort.
+// 8, 2048 bf16: 51 us, 5.6 TB/s, and 61 us with the sort.
 __global__ __launch_bounds__(256) void k_spread_rows(int64_t tokens, int top_k, int64_t units, int lw,
                                                      const int32_t* __restrict__ rows, const u32x4* __restrict__ x,
                                                      const float* __restrict__ x_scale, u32x4* __restrict__ xs,
@@ -323,7 +343,7 @@ __global__ __launch_bounds__(256) void k_dispatch_few(const int32_t* __restrict_
 #pragma unroll
     for (int b = 0; b < B; ++b) {
         const int p = b * 64 + lane;
-        k[b] = p < P ? (k[b] >= 0 && k[b] < E ? k[b] : E) * P + p : INT32_MAX;
+        k[b] = p < P ? bucket(k[b], E) * P + p : INT32_MAX;
     }
     for (int j0 = 0; j0 < top_k; j0 += J) {
         int key[J], row[J];
