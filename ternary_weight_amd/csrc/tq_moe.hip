@@ -18,7 +18,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kSortThreads = 1024;            // one workgroup's sort
-constexpr int64_t kSmallPairs = 8192;         // up to here one workgroup sorts ...
+constexpr int64_t kSmallPairs = 5120;         // up to here one workgroup sorts (4096 pairs 10.0 us with their rows of
+                                              // 1 KiB, in two launches 11.1; 5600 pairs 11.2 against 10.5) ...
 constexpr int kSmallExperts = 960;            // ... if its counters (16 waves by n_experts + 1) fit 64 KiB of LDS
 constexpr int64_t kBlockPairs = 2048;         // the two-launch sort's pairs per workgroup, at least: with 1024 threads
 constexpr int kMaxBlocks = 256;               // 65536 pairs take 10 us (256 threads and 1024 pairs: 13 us)

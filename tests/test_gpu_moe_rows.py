@@ -76,7 +76,7 @@ def test_sort(T, k, E, kind):
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
 @pytest.mark.parametrize("T,k,E", [(128, 8, 1024), (1024, 1, 960), (16, 64, 5), (1025, 1, 961), (300, 4, 1000),
                                    (256, 4, 3), (257, 4, 3), (8193, 1, 2), (66000, 8, 1024), (64, 1, 9), (65, 1, 9),
-                                   (256, 1, 40), (257, 1, 40), (64, 8, 128), (513, 1, 7)])
+                                   (256, 1, 40), (257, 1, 40), (64, 8, 128), (513, 1, 7), (640, 8, 64), (5121, 1, 64), (8192, 1, 960)])
 def test_sort_at_its_kernels_edges(T, k, E, kind):
     """Pair and expert counts on both sides of each way of sorting."""
     test_sort(T, k, E, kind)
