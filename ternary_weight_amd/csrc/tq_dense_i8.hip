@@ -362,18 +362,20 @@ __global__ __launch_bounds__(256 * KS) void k_dense_i8_tile(Args A, int tiles_m,
 }
 
 // ---------------------------------------------------------------------------
-// The kernels, and which one a product takes: the one of the least estimated
-// time, in microseconds: `base` and a smooth maximum (the 8th root of the sum
-// of 8th powers) of
+// The kernels, and which one a product takes: the one of the least estimate:
+// `base` and a smooth maximum (the 8th root of the sum of 8th powers) of
 //   rounds (setup + turn turns)     a workgroup's own latency,
 //   q (wg + busy turns)             q workgroups' work on a compute unit,
 //   stream bytes / 5.2e6            the operands and outputs, at memory's rate,
 // with `turns` the 128-column blocks of one column group, `rounds` how often
-// the resident workgroups are replaced and q the tiles per compute unit.  The
-// constants are fitted to measured times of every kernel on 401 products (M 1
-// .. 4096, N 150 .. 40000, Kin 256 .. 14336, fp32 outputs); over them the
-// choice costs 3.3% (geometric mean) against the fastest of 24 kernels
-// measured, 47% at worst (160 x 12000 x 14336).
+// the resident workgroups are replaced and q the tiles of the fullest compute
+// unit.  The constants are in microseconds, but fitted to the choice, not to
+// each time: so that over the measured times of every kernel on 1397 products
+// (M 1 .. 8192, N 150 .. 151936, Kin 128 .. 32768, half of them drawn at
+// random; fp32 outputs, weights in no cache, as in a model that runs layer by
+// layer) the choices cost least: 0.7% (geometric mean) against the fastest of
+// these kernels, 17% at worst (43 x 801 x 2272).  A fit without half of the
+// random products cost 1.2% on those.
 struct Kernel {
     void (*f32)(Args, int, int);
     void (*bf16)(Args, int, int);
@@ -387,15 +389,17 @@ struct Kernel {
     {k_dense_i8_tile<TQ_F32, FM, FN, KS, NS>, k_dense_i8_tile<TQ_BF16, FM, FN, KS, NS>, 32 * FM, 32 * FN, KS, \
      256 * KS, RES
 const Kernel kKernels[] = {
-    TQ_DENSE_FEW(4),              0.027, 1.153, 0.297, 0.000, 1.038, 2.994},     // M <= 16 only
-    TQ_DENSE_TILE(1, 1, 1, 4, 5), 0.000, 1.401, 0.114, 0.336, 0.968, 2.847},
-    TQ_DENSE_TILE(1, 1, 2, 4, 2), 0.000, 2.089, 0.180, 1.262, 1.061, 2.113},
-    TQ_DENSE_TILE(2, 2, 1, 3, 3), 0.000, 2.144, 0.232, 1.029, 1.116, 2.052},
-    TQ_DENSE_TILE(2, 2, 2, 4, 1), 0.411, 0.000, 0.326, 4.105, 1.159, 0.135},
-    TQ_DENSE_TILE(4, 4, 1, 3, 1), 0.450, 4.709, 0.014, 0.572, 1.739, 0.018},
-    TQ_DENSE_TILE(4, 8, 1, 3, 1), 0.796, 7.543, 0.226, 0.510, 1.211, 0.000},
-    TQ_DENSE_TILE(6, 8, 1, 2, 1), 0.204, 3.694, 1.123, 10.65, 1.489, 0.000},
-    TQ_DENSE_TILE(8, 8, 1, 2, 1), 0.254, 2.762, 1.331, 14.35, 1.456, 0.000},
+    TQ_DENSE_FEW(4),              0.000, 0.000, 0.003, 0.000, 1.710, 1.540},     // M <= 16 only
+    TQ_DENSE_TILE(1, 1, 1, 4, 5), 0.289, 0.896, 0.119, 1.050, 0.973, 0.209},
+    TQ_DENSE_TILE(1, 1, 2, 4, 2), 0.378, 0.001, 0.318, 2.150, 0.000, 0.182},
+    TQ_DENSE_TILE(1, 2, 2, 4, 1), 0.000, 6.510, 0.507, 0.557, 1.400, 0.436},
+    TQ_DENSE_TILE(2, 2, 1, 3, 3), 0.374, 2.290, 0.380, 0.360, 0.521, 0.000},
+    TQ_DENSE_TILE(2, 2, 2, 4, 1), 0.000, 6.800, 0.603, 2.660, 0.992, 0.417},
+    TQ_DENSE_TILE(4, 2, 1, 3, 2), 0.012, 4.600, 0.402, 2.770, 1.000, 0.001},
+    TQ_DENSE_TILE(4, 4, 1, 3, 1), 0.532, 0.852, 0.305, 4.240, 0.008, 0.715},
+    TQ_DENSE_TILE(4, 8, 1, 3, 1), 0.680, 5.470, 0.659, 5.140, 0.013, 0.000},
+    TQ_DENSE_TILE(6, 8, 1, 2, 1), 1.000, 3.770, 0.765, 7.280, 0.828, 0.000},
+    TQ_DENSE_TILE(8, 8, 1, 2, 1), 0.954, 9.660, 1.200, 0.432, 0.034, 0.000},
 };
 
 int64_t tiles_of(const Kernel& k, int64_t M, int64_t N) { return ((M + k.tm - 1) / k.tm) * ((N + k.tn - 1) / k.tn); }
@@ -404,7 +408,7 @@ double estimate(const Kernel& k, int64_t M, int64_t N, int64_t Kin, int64_t y_by
 {
     const double x = (double)tiles_of(k, M, N) / cus;
     const double turns = (double)(((Kin + 127) / 128 + k.groups - 1) / k.groups);
-    const double q = k.resident == 1 ? ceil(x) : x < 1.0 ? 1.0 : x;
+    const double q = x <= k.resident || k.resident == 1 ? ceil(x) : x;
     const double own = ceil(x / k.resident) * (k.setup + k.turn * turns), work = q * (k.wg + k.busy * turns);
     const double mem = k.stream * (double)(N * Kin + M * Kin + y_bytes) / 5.2e6;
     const auto eighth = [](double v) { return v *= v, v *= v, v * v; };
@@ -420,6 +424,8 @@ const Kernel* pick(int64_t M, int64_t N, int64_t Kin, int64_t y_bytes)
     for (size_t i = M <= 16 ? 0 : 1; i < sizeof kKernels / sizeof kKernels[0]; ++i) {
         const Kernel& k = kKernels[i];
         if (tiles_of(k, M, N) > (int64_t)UINT32_MAX / k.threads) continue;     // a launch counts its threads in 32 bits
+        if (M <= 32 && k.tm >= 128) continue;     // mostly absent tokens: at most 10% faster anywhere, 8% slower on a
+                                                  // head of 128256 rows where the estimates took one
         const double us = estimate(k, M, N, Kin, y_bytes, cus);
         if (!best || us < best_us) best = &k, best_us = us;
     }

@@ -109,7 +109,13 @@ EDGES = [(700, 1001, 3312), (300, 4097, 2320), (200, 5002, 4448), (300, 2563, 18
          (257, 2049, 2720), (70, 5002, 704), (130, 1001, 2672), (1023, 9985, 16), (1025, 9987, 176),
          (200, 30001, 960), (385, 9999, 2128), (450, 12001, 1616), (1025, 7001, 1568), (2050, 2563, 496), (70, 7001, 6816),
          (200, 2563, 7280), (450, 1001, 7504), (130, 4097, 3040), (200, 9999, 2576), (257, 7001, 4000), (700, 4097, 1520),
-         (257, 30001, 4656), (700, 12001, 672)]
+         (257, 30001, 4656), (700, 12001, 672),
+         (130, 5002, 928), (385, 9999, 1360), (385, 12001, 2464), (300, 5002, 6480), (161, 5002, 1680),
+         (90, 5002, 2464), (300, 2047, 7008), (257, 7001, 4240), (130, 2563, 2112), (200, 12001, 1680),
+         (200, 7001, 3792), (90, 4097, 2592), (33, 9999, 5216), (97, 9999, 2352), (90, 5003, 3664),
+         (257, 2047, 6960), (130, 2047, 2800), (90, 5002, 3856), (200, 5003, 1344), (450, 2047, 2496),
+         (97, 9999, 2480), (300, 5002, 4768), (33, 12001, 4112), (130, 5003, 384), (1025, 12001, 704),
+         (1500, 7001, 1344), (1025, 12001, 304), (1025, 9999, 784), (1025, 9999, 1184), (1500, 9999, 160)]
 
 
 @pytest.mark.parametrize("M,N,K", EDGES)
